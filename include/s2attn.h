@@ -221,6 +221,111 @@ S2_API s2_status s2attn_selftest_inject(int site, const void* q, const void* k, 
  * cuda_stream. Accurate to a relative 1e-4 for x in [-125, 127]. */
 S2_API s2_status s2attn_selftest_exp2(const float* x, float* y, int n, void* cuda_stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Serving: one step of a model that these kernels trained, on dense causal attention (the
+ * inference mode of the guide's "Dual-Mode" paragraph). Per step: s2attn_page_plan gives the
+ * new tokens' positions and cache slots, s2attn_rope turns q and k, s2attn_cache4_append
+ * stores k and v in 4 bits, s2attn_cache4_attn attends to all that is stored. The pages have
+ * no counterpart of the cache. Pointers are device pointers unless noted; nothing is
+ * allocated and nothing synchronises, so a step can be captured into a graph.
+ * Whole numbers that live on the device (lengths, tables, slots) cannot be checked by the
+ * host: each call says what it does where they do not fit. */
+
+/* RoPE frequencies of `rotary_dim` / 2 channel pairs, in turns per token, into the HOST array
+ * `turns` (copy it to the device once; s2attn_rope reads it there). Pair i turns by
+ * theta_i = rope_base^(-2i/rotary_dim) radians a token, divided by pi_scale (linear position
+ * interpolation; base scaling is pi_scale = 1 with a larger rope_base). original_len > 0:
+ * interpolation by parts, as YaRN defines it ("YaRN: Efficient Context Window Extension of
+ * Large Language Models", section on NTK-by-parts): a pair that makes at least fast_turns
+ * turns over original_len tokens keeps theta_i, one that makes at most slow_turns is
+ * divided by pi_scale, those between are blended linearly. */
+S2_API s2_status s2attn_rope_freqs(double* turns, int rotary_dim, double rope_base,
+                                   double pi_scale, int original_len, double slow_turns,
+                                   double fast_turns);
+
+#define S2_ROPE_INTERLEAVED 0 /* pair i is channels (2i, 2i+1): the attention calls' layout */
+#define S2_ROPE_HALF 1        /* pair i is channels (i, i + rotary_dim/2) */
+
+/* Rotary positions of q [B][N][H_q][d] and k [B][N][H_kv][d] (k and k_out NULL: q alone):
+ * pair i of the first rotary_dim channels of token (b, n) is turned by
+ * 2 pi positions[b, n] freqs[i] and multiplied by mscale; the other channels are copied.
+ * inverse != 0 turns the other way: with the same mscale, the gradient of the forward.
+ * Strides are host arrays, in elements: q, k of batch, token and head (channels are dense);
+ * pos_strides of batch (0: one row of positions for all) and token. q_out == q and
+ * k_out == k work in place; any other output is dense and overlaps no input.
+ * positions: int32, or int64 with positions64. d and rotary_dim are even, at most 256. */
+S2_API s2_status s2attn_rope(const void* q, void* q_out, const void* k, void* k_out,
+                             const void* positions, int positions64, const double* freqs, int B,
+                             int N, int H_q, int H_kv, int d, int rotary_dim,
+                             const long long* q_strides, const long long* k_strides,
+                             const long long* pos_strides, int layout, int inverse, float mscale,
+                             int dtype, void* cuda_stream);
+
+/* Block tables and slot maps of one step, on the GPU, from the requests' lengths.
+ * Request r (of R <= 4096) has cached_lens[r] tokens in the pages block_table[r][0 ..] and
+ * adds new_lens[r]. Pages of page_size tokens (16, 32, 64, 128 or 256) are taken, in the
+ * requests' order, from the end of free_pages[0 .. *free_count - 1] (n_free entries at most)
+ * and written behind the request's own; the rest of block_table stays. Written:
+ *   cu_new[R + 1]   rows of the step's tokens: request r has rows cu_new[r] .. cu_new[r+1]-1
+ *   lens[R]         cached_lens + new_lens
+ *   positions[T], slots[T]  of each row: place in the request, and page * page_size + place
+ *                   in the page; rows behind the last request: 0 and -1
+ *   counts[2]       free pages left (the next step's *free_count), requests left out
+ * A request is left out (its slots are -1, lens[r] = cached_lens[r], it takes no page) where a
+ * length is negative, max_pages columns do not hold it, its rows do not end within T, or the
+ * free pages do not suffice; with the last two, so is every later request that has rows or
+ * takes pages. Outputs other than block_table must not alias inputs. */
+S2_API s2_status s2attn_page_plan(const int* cached_lens, const int* new_lens,
+                                  const int* free_pages, const int* free_count, int* block_table,
+                                  int* cu_new, int* lens, int* positions, int* slots, int* counts,
+                                  int R, int T, int n_free, int max_pages, long long table_stride,
+                                  int page_size, void* cuda_stream);
+
+/* The 4-bit cache: n_pages pages of page_size tokens for each of H_kv heads of d channels
+ * (a multiple of 32 in [32, 256]), laid out [n_pages][H_kv][page_size / 16][20 d bytes]. A
+ * value is minimum + scale * code (0..15), one fp16 scale and minimum per 32 channels of a
+ * token's head: 5 bits a value. Bytes, or 0 for arguments that the calls would reject. Fewer
+ * than 2^31 slots; 16-byte aligned; its contents need no initialisation. */
+S2_API size_t s2attn_cache4_bytes(int n_pages, int page_size, int H_kv, int d);
+
+/* Stores k, v [T][H_kv][d] (strides of token and head in elements, multiples of 16 bytes) in
+ * the cache's slots[0 .. T-1]. Rows whose slot is negative or beyond the cache are skipped.
+ * Slots of one call must differ: rows that share one leave it undefined. Values are limited
+ * to +-65504. A NaN or infinity in the k or v of a token's head makes that (token, head) NaN
+ * for every query that attends to it, and leaves the others alone. */
+S2_API s2_status s2attn_cache4_append(const void* k, const void* v, void* cache, const int* slots,
+                                      int T, int H_kv, int d, int n_pages, int page_size,
+                                      const long long* k_strides, const long long* v_strides,
+                                      int dtype, void* cuda_stream);
+
+/* The values that slots[0 .. T-1] hold, into dense k, v [T][H_kv][d]. Slots outside the cache
+ * give zeros. */
+S2_API s2_status s2attn_cache4_read(const void* cache, const int* slots, void* k, void* v, int T,
+                                    int H_kv, int d, int n_pages, int page_size, int dtype,
+                                    void* cuda_stream);
+
+/* Bytes of workspace of s2attn_cache4_attn, for every shape. It must be zero before its first
+ * use; each call leaves it ready for the next. A workspace serves one call at a time. */
+S2_API size_t s2attn_cache4_workspace_bytes(void);
+
+/* Attention over the cache: o[t] = softmax(q[t] k^T * scale) v over request r's slots, for its
+ * rows t = cu_new[r] .. cu_new[r+1]-1 of q [T][H_q][d] (strides of token and head in elements,
+ * multiples of 16 bytes). lens[r] counts the request's stored tokens, those of this step
+ * included; its row number i of n sees the first lens[r] - (n - 1 - i): its own place and all
+ * before. Query head h uses kv head h / (H_q / H_kv). o is dense [T][H_q][d]; lse, if not
+ * NULL, is [H_q][T] float32. A row that sees no key gets o = 0 and lse = -inf; rows that no
+ * request owns stay as they were. max_new: the largest number of rows of a request, from
+ * which the kernel's tile is chosen (another value costs time, not correctness). A page
+ * number outside the cache among those a row attends to makes that row NaN; lens beyond
+ * max_pages * page_size counts as that much. */
+S2_API s2_status s2attn_cache4_attn(const void* q, const void* cache, const int* block_table,
+                                    const int* lens, const int* cu_new, void* o, float* lse,
+                                    int R, int T, int H_q, int H_kv, int d, int n_pages,
+                                    int page_size, int max_pages, long long table_stride,
+                                    const long long* q_strides, int max_new, float scale,
+                                    int dtype, void* workspace, size_t ws_bytes,
+                                    void* cuda_stream);
+
 /* Static, NUL-terminated description of a status code. */
 S2_API const char* s2attn_status_string(int status);
 

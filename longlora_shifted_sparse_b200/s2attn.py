@@ -5,7 +5,8 @@ Two layers:
 * the C ABI under its own names (``s2attn_fwd``, ``s2attn_bwd``, ...), taking raw device
   pointers and sizes exactly like ``include/s2attn.h``;
 * torch conveniences (``forward``, ``backward``, ``S2AttnFunction``) that allocate outputs
-  and the workspace with torch and pass their pointers and the current CUDA stream.
+  and the workspace with torch and pass their pointers and the current CUDA stream; and the
+  serving step (``page_plan``, ``rope``, ``cache4_append``, ``cache4_attention``).
 
 Importing this module raises ImportError when the library has not been built: there is no
 fallback implementation.
@@ -14,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libs2attn.so")
@@ -24,6 +26,8 @@ S2_OK, S2_ERR_NULL, S2_ERR_SHAPE, S2_ERR_DTYPE, S2_ERR_HEADDIM, S2_ERR_ALIGN, \
 S2_BF16, S2_FP32 = 0, 1
 S2_CAUSAL, S2_SHIFT_HALF, S2_SHIFT_ALTERNATE, S2_SHIFT_NONE = 0x01, 0x00, 0x10, 0x20
 S2_INJECT_FWD, S2_INJECT_DKDV = 1, 2
+S2_ROPE_INTERLEAVED, S2_ROPE_HALF = 0, 1
+ROPE_LAYOUTS = {"interleaved": S2_ROPE_INTERLEAVED, "half": S2_ROPE_HALF}
 SHIFT_PATTERNS = {"half": S2_SHIFT_HALF, "alternate": S2_SHIFT_ALTERNATE, "none": S2_SHIFT_NONE}
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # S2ATTN_NOALLOC_SCRATCH_BYTES
 
@@ -59,6 +63,23 @@ _lib.s2attn_selftest_exp2.argtypes = [_vp, _vp, _i, _vp]
 _lib.s2attn_selftest_exp2.restype = _i
 _lib.s2attn_device_status.argtypes = [_vp, _sz, _vp]
 _lib.s2attn_device_status.restype = _i
+_ll, _dbl = ctypes.c_longlong, ctypes.c_double
+_lib.s2attn_rope_freqs.argtypes = [ctypes.POINTER(_dbl), _i, _dbl, _dbl, _i, _dbl, _dbl]
+_lib.s2attn_rope_freqs.restype = _i
+_lib.s2attn_rope.argtypes = [_vp] * 5 + [_i, _vp] + [_i] * 6 + [_vp] * 3 + [_i, _i, _f, _i, _vp]
+_lib.s2attn_rope.restype = _i
+_lib.s2attn_page_plan.argtypes = [_vp] * 10 + [_i] * 4 + [_ll, _i, _vp]
+_lib.s2attn_page_plan.restype = _i
+_lib.s2attn_cache4_bytes.argtypes = [_i] * 4
+_lib.s2attn_cache4_bytes.restype = _sz
+_lib.s2attn_cache4_append.argtypes = [_vp] * 4 + [_i] * 5 + [_vp, _vp, _i, _vp]
+_lib.s2attn_cache4_append.restype = _i
+_lib.s2attn_cache4_read.argtypes = [_vp] * 4 + [_i] * 6 + [_vp]
+_lib.s2attn_cache4_read.restype = _i
+_lib.s2attn_cache4_workspace_bytes.argtypes = []
+_lib.s2attn_cache4_workspace_bytes.restype = _sz
+_lib.s2attn_cache4_attn.argtypes = [_vp] * 7 + [_i] * 8 + [_ll, _vp, _i, _f, _i, _vp, _sz, _vp]
+_lib.s2attn_cache4_attn.restype = _i
 _lib.s2attn_status_string.argtypes = [_i]
 _lib.s2attn_status_string.restype = ctypes.c_char_p
 _lib.s2attn_profile_enable.argtypes = [_i]
@@ -83,6 +104,14 @@ s2attn_device_status = _lib.s2attn_device_status
 s2attn_selftest_wait_timeout = _lib.s2attn_selftest_wait_timeout
 s2attn_selftest_inject = _lib.s2attn_selftest_inject
 s2attn_selftest_exp2 = _lib.s2attn_selftest_exp2
+s2attn_rope_freqs = _lib.s2attn_rope_freqs
+s2attn_rope = _lib.s2attn_rope
+s2attn_page_plan = _lib.s2attn_page_plan
+s2attn_cache4_bytes = _lib.s2attn_cache4_bytes
+s2attn_cache4_append = _lib.s2attn_cache4_append
+s2attn_cache4_read = _lib.s2attn_cache4_read
+s2attn_cache4_workspace_bytes = _lib.s2attn_cache4_workspace_bytes
+s2attn_cache4_attn = _lib.s2attn_cache4_attn
 s2attn_profile_enable = _lib.s2attn_profile_enable
 s2attn_profile_num_kernels = _lib.s2attn_profile_num_kernels
 s2attn_profile_dropped = _lib.s2attn_profile_dropped
@@ -265,3 +294,280 @@ def s2_attention(q, k, v, G: int, pi_scale: float, rope_base: float = 10000.0,
     if _fn is None:
         _fn = _make_function()
     return _fn.apply(q, k, v, G, pi_scale, rope_base, causal, shift)
+
+
+# ----------------------------------------------------------------------------- serving
+#
+# Calls on tensors of another device than the current one make that device current for the
+# launch; work goes to that device's current stream.
+
+def _call(device, fn, *args) -> None:
+    import torch
+    if device.index == torch.cuda.current_device():
+        check(fn(*args, _stream_ptr(device)))
+    else:
+        with torch.cuda.device(device):
+            check(fn(*args, _stream_ptr(device)))
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _ints(t, name, device, shape=None):
+    """A dense int32 CUDA tensor of this device (and shape)."""
+    import torch
+    if t.dtype is not torch.int32:
+        raise TypeError("%s must be int32, got %s" % (name, t.dtype))
+    _need(t.device == device, "%s is on %s, not on %s" % (name, t.device, device))
+    _need(t.is_contiguous() and (shape is None or tuple(t.shape) == shape),
+          "%s must be dense%s" % (name, "" if shape is None else " with shape %s" % (shape,)))
+    return t.data_ptr()
+
+
+_ll2, _ll3 = _ll * 2, _ll * 3
+
+
+def rope_freqs(rotary_dim: int, rope_base: float = 10000.0, pi_scale: float = 1.0,
+               original_len: int = 0, slow_turns: float = 1.0, fast_turns: float = 32.0,
+               device="cuda"):
+    """Frequencies of the channel pairs in turns per token: float64 [rotary_dim / 2] on `device`,
+    made once and kept for ``rope``. pi_scale: linear position interpolation; base scaling is a
+    larger rope_base; original_len > 0 interpolates by parts (a pair that makes fast_turns or
+    more over original_len tokens is kept, slow_turns or fewer interpolated, blended between)."""
+    import torch
+    host = (_dbl * max(1, int(rotary_dim) // 2))()
+    check(s2attn_rope_freqs(host, rotary_dim, rope_base, pi_scale, original_len, slow_turns,
+                            fast_turns))
+    return torch.tensor(list(host), dtype=torch.float64).to(device)
+
+
+def _rope_rows(x, name):
+    """x as [B, N, H, d] (a [T, H, d] tensor is one batch entry) with dense channels."""
+    _need(x.dim() in (3, 4), "%s must be [T, H, d] or [B, N, H, d], got %s" % (name, tuple(x.shape)))
+    x = x if x.dim() == 4 else x.unsqueeze(0)
+    return x if x.stride(-1) == 1 and x.data_ptr() % 16 == 0 else x.contiguous()
+
+
+def _rope_launch(q, k, positions, freqs, layout, mscale, inverse, in_place):
+    import torch
+    dt = _dtype_code(q)
+    q4 = _rope_rows(q, "q")
+    B, N, Hq, d = q4.shape
+    pos = positions if positions.dim() == 2 else positions.unsqueeze(0)
+    if pos.dtype not in (torch.int32, torch.int64):
+        raise TypeError("positions must be int32 or int64, got %s" % positions.dtype)
+    if freqs.dtype != torch.float64:
+        raise TypeError("freqs must be float64 (see rope_freqs), got %s" % freqs.dtype)
+    _need(pos.dim() == 2 and pos.shape[1] == N and pos.shape[0] in (1, B),
+          "positions must be [N] or [B, N], got %s" % (tuple(positions.shape),))
+    _need(freqs.dim() == 1 and freqs.is_contiguous(), "freqs must be one dense row")
+    _need(q.device == pos.device == freqs.device, "q, positions and freqs must share a device")
+    out = q if in_place else torch.empty_like(q4, memory_format=torch.contiguous_format)
+    _need(not in_place or q4.data_ptr() == q.data_ptr(),
+          "in place needs dense, 16-byte aligned channels")
+    k4 = kout = None
+    if k is not None:
+        _need(k.dtype == q.dtype and k.device == q.device, "q and k must share dtype and device")
+        k4 = _rope_rows(k, "k")
+        _need(k4.shape[:2] == q4.shape[:2] and k4.shape[3] == d and k.dim() == q.dim(),
+              "q %s and k %s must share all but heads" % (tuple(q.shape), tuple(k.shape)))
+        kout = k if in_place else torch.empty_like(k4, memory_format=torch.contiguous_format)
+        _need(not in_place or k4.data_ptr() == k.data_ptr(),
+              "in place needs dense, 16-byte aligned channels")
+    if q4.numel() or (k4 is not None and k4.numel()):
+        _call(q.device, s2attn_rope, q4.data_ptr(), out.data_ptr(),
+              None if k is None else k4.data_ptr(), None if k is None else kout.data_ptr(),
+              pos.data_ptr(), pos.dtype == torch.int64, freqs.data_ptr(), B, N, Hq,
+              0 if k is None else k4.shape[2], d, 2 * freqs.numel(), _ll3(*q4.stride()[:3]),
+              None if k is None else _ll3(*k4.stride()[:3]),
+              _ll2(0 if pos.shape[0] == 1 else pos.stride(0), pos.stride(1)),
+              ROPE_LAYOUTS[layout], inverse, mscale, dt)
+    return out.view(q.shape), None if k is None else kout.view(k.shape)
+
+
+_rope_fn = None
+
+
+def _make_rope_function():
+    import torch
+
+    class RopeFunction(torch.autograd.Function):
+        """Autograd wrapper: the gradient is the same rotation the other way round."""
+
+        @staticmethod
+        def forward(ctx, q, k, positions, freqs, layout, mscale):
+            ctx.save_for_backward(positions, freqs)
+            ctx.args = (layout, mscale)
+            return _rope_launch(q, k, positions, freqs, layout, mscale, False, False)
+
+        @staticmethod
+        def backward(ctx, dq, dk):
+            positions, freqs = ctx.saved_tensors
+            dq, dk = _rope_launch(dq, dk, positions, freqs, *ctx.args, True, False)
+            return dq, dk, None, None, None, None
+
+    return RopeFunction
+
+
+def rope(q, k, positions, freqs, layout: str = "interleaved", mscale: float = 1.0,
+         in_place: bool = False):
+    """Rotary positions of q [B,N,Hq,d] and k [B,N,Hkv,d] (or [T,H,d]; k may be None) -> (q', k').
+
+    positions: int32 or int64, [N] (or [T]) or [B, N]; freqs: ``rope_freqs``, whose length gives
+    the rotated channels, the first 2 * len(freqs); the rest pass through. layout: pair i is
+    channels (2i, 2i+1) ("interleaved", as in the attention calls) or (i, i + half)
+    ("half"). mscale multiplies the rotated channels. Differentiable in q and k;
+    in_place=True overwrites them instead and has no gradient."""
+    import torch
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError("layout must be one of %s, got %r" % (sorted(ROPE_LAYOUTS), layout))
+    grad = torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad))
+    if not grad:
+        return _rope_launch(q, k, positions, freqs, layout, mscale, False, in_place)
+    _need(not in_place, "in_place=True has no gradient")
+    global _rope_fn
+    if _rope_fn is None:
+        _rope_fn = _make_rope_function()
+    return _rope_fn.apply(q, k, positions, freqs, layout, mscale)
+
+
+class PagePlan(NamedTuple):
+    """What ``page_plan`` gives: see there."""
+    cu_new: "torch.Tensor"
+    lens: "torch.Tensor"
+    positions: "torch.Tensor"
+    slots: "torch.Tensor"
+    free_count: "torch.Tensor"
+    left_out: "torch.Tensor"
+
+
+def page_plan(cached_lens, new_lens, free_pages, free_count, block_table, page_size: int,
+              max_tokens: int) -> PagePlan:
+    """Pages, positions and slots of one step's new tokens, from the requests' lengths.
+
+    cached_lens, new_lens [R], free_pages [F], free_count [1], block_table [R, max_pages]: int32
+    CUDA tensors. The pages that the new tokens need are taken from the end of
+    free_pages[:free_count] and written into block_table (in place, behind each request's own).
+    Returns cu_new [R+1], lens [R] (cached + new), positions and slots [max_tokens] (slots -1
+    in rows that no request owns), free_count [1] (what is left) and left_out [1]: the number
+    of requests that did not fit (too long for the table or for max_tokens, or no pages left),
+    whose slots are -1 and whose lengths stay."""
+    import torch
+    dev = cached_lens.device
+    R = cached_lens.numel()
+    c, n = _ints(cached_lens, "cached_lens", dev, (R,)), _ints(new_lens, "new_lens", dev, (R,))
+    f, fc = _ints(free_pages, "free_pages", dev), _ints(free_count, "free_count", dev, (1,))
+    if block_table.dtype is not torch.int32:
+        raise TypeError("block_table must be int32, got %s" % block_table.dtype)
+    _need(block_table.device == dev and block_table.dim() == 2 and block_table.shape[0] == R and
+          (block_table.stride(1) == 1 or block_table.shape[1] <= 1),
+          "block_table must be [R, max_pages] on %s with dense rows" % dev)
+    out = torch.empty(2 * R + 1 + 2 * max_tokens + 2, dtype=torch.int32, device=dev)
+    cu, lens, pos, slots, free_left, left_out = out.split((R + 1, R, max_tokens, max_tokens, 1, 1))
+    p, b = out.data_ptr(), 4 * (2 * R + 1)
+    _call(dev, s2attn_page_plan, c, n, f, fc, block_table.data_ptr(), p, p + 4 * (R + 1), p + b,
+          p + b + 4 * max_tokens, p + b + 8 * max_tokens, R, max_tokens, free_pages.numel(),
+          block_table.shape[1], max(block_table.stride(0), block_table.shape[1]), page_size)
+    return PagePlan(cu, lens, pos, slots, free_left, left_out)
+
+
+def cache4(n_pages: int, page_size: int, Hkv: int, d: int, device="cuda"):
+    """An empty 4-bit cache: uint8 [n_pages, Hkv, page_size / 16, 20 d]."""
+    import torch
+    if s2attn_cache4_bytes(n_pages, page_size, Hkv, d) == 0:
+        raise S2Error(S2_ERR_SHAPE)
+    return torch.zeros(n_pages, Hkv, page_size // 16, 20 * d, dtype=torch.uint8, device=device)
+
+
+def _cache4_shape(cache):
+    """(n_pages, page_size, Hkv, d) of a cache tensor."""
+    import torch
+    _need(cache.dtype is torch.uint8 and cache.dim() == 4 and cache.is_contiguous() and
+          cache.shape[3] % 20 == 0, "cache must be a tensor that cache4() made")
+    n_pages, Hkv, subs, width = cache.shape
+    return n_pages, 16 * subs, Hkv, width // 20
+
+
+def cache4_append(k, v, cache, slots) -> None:
+    """Stores k, v [T, Hkv, d] in the cache's slots (int32 [T]; rows with a negative slot, or one
+    beyond the cache, are skipped; the others must differ)."""
+    n_pages, P, Hkv, d = _cache4_shape(cache)
+    _need(k.dim() == 3 and k.shape == v.shape and tuple(k.shape[1:]) == (Hkv, d),
+          "k %s and v %s must be [T, %d, %d]" % (tuple(k.shape), tuple(v.shape), Hkv, d))
+    _need(k.dtype == v.dtype and k.device == v.device == cache.device,
+          "k, v must share a dtype, and their device with the cache")
+    T, dt = k.shape[0], _dtype_code(k)
+    at = _ints(slots, "slots", cache.device, (T,))
+    if T == 0:
+        return
+    k, v = (x if x.stride(2) == 1 and (x.data_ptr() | (x.stride(0) | x.stride(1)) * x.element_size())
+            % 16 == 0 else x.contiguous() for x in (k, v))
+    _call(cache.device, s2attn_cache4_append, k.data_ptr(), v.data_ptr(), cache.data_ptr(), at, T,
+          Hkv, d, n_pages, P, _ll2(*k.stride()[:2]), _ll2(*v.stride()[:2]), dt)
+
+
+def cache4_read(cache, slots, dtype=None):
+    """(k, v) [T, Hkv, d] that the slots (int32 [T]) hold, in bfloat16 or float32; slots outside
+    the cache give zeros."""
+    import torch
+    n_pages, P, Hkv, d = _cache4_shape(cache)
+    T = slots.numel()
+    at = _ints(slots, "slots", cache.device, (T,))
+    k = torch.empty(T, Hkv, d, dtype=dtype or torch.bfloat16, device=cache.device)
+    v = torch.empty_like(k)
+    if T:
+        _call(cache.device, s2attn_cache4_read, cache.data_ptr(), at, k.data_ptr(), v.data_ptr(), T,
+              Hkv, d, n_pages, P, _dtype_code(k))
+    return k, v
+
+
+def cache4_workspace(device="cuda"):
+    """The workspace of ``cache4_attention``: one for each stream that runs it, kept between calls."""
+    import torch
+    return torch.zeros(s2attn_cache4_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def cache4_attention(q, cache, block_table, lens, cu_new, max_new: int, scale=None, ws=None,
+                     out=None, return_lse: bool = False):
+    """Attention of a step's tokens over all that the cache holds of their requests.
+
+    q [T, Hq, d]; request r has its rows cu_new[r] .. cu_new[r+1]-1 (int32 [R+1]), the pages
+    block_table[r] (int32 [R, max_pages]) and lens[r] stored tokens, those of this step
+    included (int32 [R]); a row sees its own place and all before. max_new: the largest number
+    of rows of a request (known to the caller; it picks the kernel's tile). scale: 1 / sqrt(d)
+    by default. ws: ``cache4_workspace``, made anew where it is None. Returns o [T, Hq, d]
+    (out, if given, whose rows that no request owns stay as they were), or (o, lse) with lse
+    [Hq, T]. A row that sees no key gets 0 and -inf."""
+    import torch
+    n_pages, P, Hkv, d = _cache4_shape(cache)
+    dev = cache.device
+    _need(q.dim() == 3 and q.shape[2] == d and q.device == dev,
+          "q must be [T, Hq, %d] on %s, got %s on %s" % (d, dev, tuple(q.shape), q.device))
+    T, Hq, _ = q.shape
+    dt, R = _dtype_code(q), lens.numel()
+    ln, cu = _ints(lens, "lens", dev, (R,)), _ints(cu_new, "cu_new", dev, (R + 1,))
+    if block_table.dtype is not torch.int32:
+        raise TypeError("block_table must be int32, got %s" % block_table.dtype)
+    _need(block_table.device == dev and block_table.dim() == 2 and block_table.shape[0] == R and
+          (block_table.stride(1) == 1 or block_table.shape[1] <= 1),
+          "block_table must be [R, max_pages] on %s with dense rows" % dev)
+    if q.stride(2) != 1 or (q.data_ptr() | (q.stride(0) | q.stride(1)) * q.element_size()) % 16:
+        q = q.contiguous()
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
+    else:
+        _need(out.shape == q.shape and out.dtype == q.dtype and out.device == dev and
+              out.is_contiguous(), "out must be a dense tensor like q")
+    lse = torch.empty((Hq, T), dtype=torch.float32, device=dev) if return_lse else None
+    if ws is None:
+        ws = cache4_workspace(dev)
+    _need(ws.device == dev, "ws is on %s, not on %s" % (ws.device, dev))
+    if T:
+        _call(dev, s2attn_cache4_attn, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), ln, cu,
+              out.data_ptr(), None if lse is None else lse.data_ptr(), R, T, Hq, Hkv, d, n_pages, P,
+              block_table.shape[1], max(block_table.stride(0), block_table.shape[1]),
+              _ll2(q.stride(0), q.stride(1)), max_new, d ** -0.5 if scale is None else scale, dt,
+              ws.data_ptr(), ws.numel())
+    return (out, lse) if return_lse else out
