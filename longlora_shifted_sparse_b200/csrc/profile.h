@@ -23,6 +23,7 @@ enum KernelId {
   kPagePlan,
   kCache4Append,
   kCache4Read,
+  kCache4Attn,
   kCache4AttnSimt,
   kNumKernels
 };
@@ -30,7 +31,7 @@ enum KernelId {
 inline const char* const kKernelNames[kNumKernels] = {
     "rope_table", "rope_pi", "fwd_tc", "fwd_simt", "bwd_rowsum", "bwd_dkdv_tc", "bwd_dq_tc",
     "bwd_dq_simt", "bwd_dkdv_simt", "rope", "page_plan", "cache4_append", "cache4_read",
-    "cache4_attn_simt"};
+    "cache4_attn", "cache4_attn_simt"};
 
 struct Record {
   int id;

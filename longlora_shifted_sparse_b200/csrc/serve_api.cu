@@ -35,6 +35,12 @@ bool cache_ok(int n_pages, int page_size) {
   return n_pages > 0 && (long long)n_pages * page_size <= 0x7fffffffLL;
 }
 
+// The attention's workspace: the arrival counters, then the parts.
+constexpr size_t kCounterBytes = (kCache4MaxCtas * sizeof(unsigned) + 255) / 256 * 256;
+
+// Tensor-core kernel: bf16 and a head dim that is a whole number of its wide loads.
+bool cache4_tc(int d, int dt) { return dt == S2_BF16 && (d == 64 || d == 128 || d == 256); }
+
 }  // namespace
 }  // namespace s2
 
@@ -183,7 +189,9 @@ s2_status s2attn_cache4_read(const void* cache, const int* slots, void* k, void*
       timed_launch(kCache4Read, s, [&] { return launch_cache4_read(a, dtype == S2_BF16, s); }));
 }
 
-size_t s2attn_cache4_workspace_bytes(void) { return 256; }
+size_t s2attn_cache4_workspace_bytes(void) {
+  return kCounterBytes + (size_t)2 * kCache4MaxCtas * (kCache4PartFloats + 2 * kCache4PartRows) * sizeof(float);
+}
 
 s2_status s2attn_cache4_attn(const void* q, const void* cache, const int* block_table,
                              const int* lens, const int* cu_new, void* o, float* lse, int R, int T,
@@ -194,7 +202,8 @@ s2_status s2attn_cache4_attn(const void* q, const void* cache, const int* block_
   if (!q || !cache || !block_table || !lens || !cu_new || !o || !q_strides) return S2_ERR_NULL;
   if (!dtype_ok(dtype)) return S2_ERR_DTYPE;
   if (R <= 0 || T <= 0 || H_q <= 0 || H_kv <= 0 || H_q % H_kv || H_q > 65535 || max_pages <= 0 ||
-      table_stride < max_pages || max_new <= 0 || !cache_ok(n_pages, page_size))
+      table_stride < max_pages || max_new <= 0 || (long long)T * H_q > 0x7fffffffLL ||
+      !cache_ok(n_pages, page_size))
     return S2_ERR_SHAPE;
   if (!headdim32_ok(d)) return S2_ERR_HEADDIM;
   const int shift = page_shift(page_size);
@@ -212,6 +221,12 @@ s2_status s2attn_cache4_attn(const void* q, const void* cache, const int* block_
   a.n_pages = n_pages; a.max_pages = max_pages; a.max_new = max_new; a.scale = scale;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool bf16 = dtype == S2_BF16;
+  if (cache4_tc(d, dtype)) {
+    a.counters = static_cast<unsigned*>(workspace);
+    a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
+    a.part_ml = a.part_o + (size_t)2 * kCache4MaxCtas * kCache4PartFloats;
+    return to_status(timed_launch(kCache4Attn, s, [&] { return launch_cache4_attn(a, s); }));
+  }
   return to_status(timed_launch(kCache4AttnSimt, s, [&] { return launch_cache4_attn_simt(a, bf16, s); }));
 }
 
