@@ -1,0 +1,852 @@
+// Attention over the 4-bit cache for many query rows at once (chunks of prompts), on the
+// 5th-generation tensor cores.
+//
+// O = softmax(Q K^T * scale) V for tiles of 256 query rows of one (request, kv head): the heads
+// that share it, times the request's tokens, in two MMA tiles of 128 rows (A, B) that share every
+// dequantised key and value. Bound by the tensor cores and, at their speed, by the softmax and
+// the dequantisation beside them; the cache's own bytes are read once per 256 rows.
+//
+// Roles (640 threads, 96 registers each):
+//   warp 0        MMA issuer and TMEM owner. Per tile of 128 keys: PV_A(j-1), QK_A(j), PV_B(j-1),
+//                 QK_B(j), so that one tile's softmax runs under the other's MMAs.
+//   warps 1..3    copies and dequantisation. Sixteen tokens' k (or v) are one contiguous piece of
+//                 10 d bytes, fetched by a bulk copy into the warp's ring of kRing; then
+//                 minimum + scale * code in fp16 is written as the MMAs' 128-byte-swizzled operands (K
+//                 rows of channels; V the same, read by the MMA transposed). K runs one tile
+//                 ahead of V, as their buffers come free. Channels lie in the order 0 4 1 5 2 6 3 7
+//                 within each eight, the order in which two codes come out of a word together:
+//                 Q is written in the same order, and O is put right when it is stored.
+//   warps 4..19   softmax: a row (TMEM lane) is shared by two warps, 64 of the 128 scores each.
+//                 They also bring Q to fp16 (a power of two per row makes it fit, and returns in
+//                 the scores' factor) and store O.
+// fp16 holds k and v to half a step 2^-12 of the value (the codes are 4 bits wide) and P to 2^-12
+// of itself; scores, maxima, sums and O are fp32.
+// The running maximum is kept as an integer 4 below the row's (P then uses fp16's range) and moves
+// only when a score exceeds it by 12, so that O is rescaled, exactly, a few times a row.
+//
+// Work is steps of 128 keys, laid on one line over (request, kv head, tile) with the steps that the
+// tile's last row sees; every CTA takes an equal run of the line. A tile that several CTAs share
+// leaves parts (sums and maxima in fp32) that a second launch joins in the order of the runs.
+// Every wait is bounded; on expiry the status word is set and the CTA drains.
+#include <math.h>
+
+#include "cache4.cuh"
+#include "common.cuh"
+#include "serve.h"
+#include "sm100.cuh"
+
+namespace s2 {
+namespace {
+
+using namespace sm100;
+
+constexpr int kRows = 128, kKeys = 128, kThreads = 640;
+constexpr int kFillWarps = 3, kRing = 6;      // pieces in flight of each dequantising warp
+constexpr uint32_t kTmemCols = 512;
+constexpr float kBelow = 4.f, kGrow = 12.f;   // log2 units
+
+template <int D>
+struct Layout {
+  static constexpr uint32_t tile = kKeys * D * 2;       // an operand tile of 128 rows
+  static constexpr uint32_t half = kKeys * 128;         // its first 64 channels
+  static constexpr uint32_t piece = 10 * D;             // 16 tokens of k, or of v
+  static constexpr uint32_t q = 0, k = 2 * tile, v = 4 * tile, ring = 6 * tile;
+  static constexpr uint32_t bytes = ring + kFillWarps * kRing * piece + 1024;
+};
+
+// The line of work: requests in order; in a request kv heads, then tiles of 256 rows, then steps.
+struct Walk {
+  int group, r, row0, n, held, tiles, h, t;
+  int q, rem;          // ((t + 1) * 256 - 1) divided by group: the tile's last token, unless it is cut
+
+  __device__ __forceinline__ void request(const Cache4AttnArgs& a, int at) {
+    r = at;
+    const int begin = a.cu[r], end = a.cu[r + 1];
+    row0 = begin;
+    n = begin >= 0 && end > begin && end <= a.T ? end - begin : 0;
+    held = (int)min((long long)max(a.lens[r], 0), (long long)a.max_pages << a.page_shift);
+    tiles = (int)(((long long)n * group + 2 * kRows - 1) / (2 * kRows));
+    first_tile();
+  }
+  __device__ __forceinline__ void first_tile() {
+    t = 0;
+    q = (2 * kRows - 1) / group;
+    rem = (2 * kRows - 1) - q * group;
+  }
+  __device__ __forceinline__ void next_tile() {
+    t++;
+    q += (2 * kRows) / group;
+    rem += (2 * kRows) % group;
+    if (rem >= group) {
+      rem -= group;
+      q++;
+    }
+  }
+  __device__ __forceinline__ int sees() const {  // keys of the tile's last row
+    return max(0, held - (n - 1 - min(q, n - 1)));
+  }
+  // a tile that sees nothing still has its rows written
+  __device__ __forceinline__ int steps() const { return max(1, (int)(((unsigned)sees() + kKeys - 1) / kKeys)); }
+  __device__ __forceinline__ long long head_steps() {  // of all tiles of one head; ends at tile 0
+    long long sum = 0;
+    for (first_tile(); t < tiles; next_tile()) sum += steps();
+    first_tile();
+    return sum;
+  }
+  __device__ __forceinline__ void next_unit(const Cache4AttnArgs& a) {
+    next_tile();
+    if (t < tiles) return;
+    first_tile();
+    if (++h < a.Hkv) return;
+    h = 0;
+    do {
+      r++;
+      if (r >= a.R) return;
+      request(a, r);
+    } while (tiles == 0);
+  }
+  __device__ __forceinline__ int rows() const { return min(2 * kRows, n * group - t * 2 * kRows); }
+};
+
+// A warp's place on the line. In shared memory: inside a unit its registers are needed elsewhere.
+struct Place {
+  Walk wk;
+  int s_begin;
+  long long left, at, chunk;   // steps to go; where the unit begins on the line; steps of a CTA
+
+  // steps of this unit that are the CTA's own
+  __device__ __forceinline__ int steps() const { return (int)min((long long)wk.steps() - s_begin, left); }
+  __device__ __forceinline__ void next(const Cache4AttnArgs& a, int lane) {
+    __syncwarp();
+    if (lane == 0) {
+      const int n = steps();
+      at += wk.steps();
+      left -= n;
+      s_begin = 0;
+      wk.next_unit(a);
+    }
+    __syncwarp();
+  }
+};
+
+struct Shared {
+  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_full[2], o_final[2], drain;
+  uint64_t ring_full[kFillWarps][kRing];
+  AbortState abort;
+  uint32_t tmem;
+  float xmax[2][2][2][kRows], xq[2][2][kRows], xsum[2][kRows];
+  int pages[kFillWarps][64];
+  Place place[kThreads / 32];
+  long long scan[kThreads / 32];
+  long long line0;           // where the found unit begins on the line
+  int find_r, find_h, find_t, found;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// 1024 + code, and 64 + code, of a word's codes 0 and 4, and 1 and 5, in fp16.
+__device__ __forceinline__ uint32_t codes04(uint32_t x) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(r) : "r"(x), "r"(0x64006400u));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes15(uint32_t x) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x00f000f0, %2, 0xea;" : "=r"(r) : "r"(x), "r"(0x54005400u));
+  return r;
+}
+// Eight values of a word, in the order 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ uint4 values8(uint32_t x, uint32_t scale, uint32_t low) {
+  const uint32_t y = x >> 8;
+  return make_uint4(hfma2(hsub2(codes04(x), 0x64006400u), scale, low),
+                    hfma2(hsub2(codes15(x), 0x54005400u), scale, low),
+                    hfma2(hsub2(codes04(y), 0x64006400u), scale, low),
+                    hfma2(hsub2(codes15(y), 0x54005400u), scale, low));
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void st_shared16(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void ld_shared(uint32_t at, uint32_t (&w)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "");
+  if constexpr (N == 1)
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+  else
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(at));
+}
+
+// kind::f16 with fp16 operands and an fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Max of a thread's 64 scores, as a tree of three-input maxima.
+__device__ __forceinline__ float max64(const uint32_t (&x0)[32], const uint32_t (&x1)[32]) {
+  float v[64];
+#pragma unroll
+  for (int c = 0; c < 32; c++) {
+    v[c] = __uint_as_float(x0[c]);
+    v[32 + c] = __uint_as_float(x1[c]);
+  }
+  float m1[22];
+#pragma unroll
+  for (int c = 0; c < 21; c++) m1[c] = fmax3(v[3 * c], v[3 * c + 1], v[3 * c + 2]);
+  m1[21] = v[63];
+  float m2[8];
+#pragma unroll
+  for (int c = 0; c < 7; c++) m2[c] = fmax3(m1[3 * c], m1[3 * c + 1], m1[3 * c + 2]);
+  m2[7] = m1[21];
+  return fmax3(fmax3(m2[0], m2[1], m2[2]), fmax3(m2[3], m2[4], m2[5]), fmaxf(m2[6], m2[7]));
+}
+
+// P = exp2(S * factor + shift) for 64 scores, as fp16 pairs over the first 32 of their columns of
+// S; returns the sum of P.
+__device__ __forceinline__ float write_p64(const uint32_t (&x0)[32], const uint32_t (&x1)[32], float factor,
+                                           float shift, uint32_t tS) {
+  const uint64_t f2 = f2pack(factor, factor), s2 = f2pack(shift, shift);
+  uint64_t acc = f2pack(0.f, 0.f);
+#pragma unroll
+  for (int ch = 0; ch < 2; ch++) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int c = 0; c < 16; c++) {
+      const float u0 = __uint_as_float(ch ? x1[2 * c] : x0[2 * c]);
+      const float u1 = __uint_as_float(ch ? x1[2 * c + 1] : x0[2 * c + 1]);
+      float a0, a1;
+      f2unpack(ffma2(f2pack(u0, u1), f2, s2), a0, a1);
+      const float p0 = ex2(a0), p1 = ex2(a1);
+      acc = fadd2(acc, f2pack(p0, p1));
+      pk[c] = pack_half2(p0, p1);
+    }
+    tmem_st16(tS + ch * 16, pk);
+  }
+  float r0, r1;
+  f2unpack(acc, r0, r1);
+  return r0 + r1;
+}
+
+// Brings the 64 P that a thread wrote to a maximum that moved, by an exact power of two.
+__device__ __forceinline__ void scale_p64(uint32_t tS, float f) {
+  uint32_t x[32];
+  tmem_ld32(tS, x);
+  tmem_wait_ld();
+#pragma unroll
+  for (int c = 0; c < 32; c++) {
+    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[c]));
+    x[c] = pack_half2(y.x * f, y.y * f);
+  }
+  tmem_st32(tS, x);
+}
+
+// 2^k for an integral k <= 0 (k = -inf gives 0), exact.
+__device__ __forceinline__ float exp2_int(float k) {
+  return k < -126.f ? 0.f : __int_as_float((static_cast<int>(k) + 127) << 23);
+}
+
+// A thread's 64 scores; those of keys from `seen` on (counted from its first) become -inf.
+__device__ __forceinline__ void load_s64(uint32_t tS, bool cut, int seen, uint32_t (&x0)[32], uint32_t (&x1)[32]) {
+  tmem_ld32(tS, x0);
+  tmem_ld32(tS + 32, x1);
+  tmem_wait_ld();
+  if (cut) {
+    const uint32_t ninf = 0xff800000u;
+#pragma unroll
+    for (int c = 0; c < 32; c++) {
+      x0[c] = c < seen ? x0[c] : ninf;
+      x1[c] = 32 + c < seen ? x1[c] : ninf;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ copies and dequantisation
+
+// Pieces of a unit of n tiles: phase 0 is K_0, then K_1, V_0, K_2, V_1 .. K_{n-1}, V_{n-2}, V_{n-1};
+// eight pieces a phase, dealt to the warps in turn.
+__device__ __forceinline__ bool phase_is_k(int p, int n) { return p == 0 || ((p & 1) && p != 2 * n - 1); }
+__device__ __forceinline__ int phase_tile(int p, int n) {
+  return p == 0 ? 0 : p == 2 * n - 1 ? n - 1 : (p & 1) ? (p + 1) / 2 : p / 2 - 1;
+}
+
+template <int D>
+__device__ __forceinline__ void fill(const Cache4AttnArgs& a, Shared& sh, uint32_t smem, Place& place,
+                                     const Abort ab) {
+  using L = Layout<D>;
+  constexpr int NG = D / 32;
+  const int w = (threadIdx.x >> 5) - 1, lane = threadIdx.x & 31;
+  const int c = lane & 3, u8 = ((lane >> 2) & 1) * 4 + (lane >> 3);
+  const uint32_t ring = smem + L::ring + w * kRing * L::piece;
+  int loads = 0, used = 0;       // pieces copied and consumed by this warp, over all units
+  uint32_t bad = 0;              // a bit a ring slot: nothing was copied (a page outside the cache)
+  int tiles_done = 0;            // tiles of earlier units
+  bool ok = true;
+  while (place.left > 0 && ok) {
+    const int s_begin = place.s_begin, n = place.steps(), held = place.wk.held;
+    const int* table = a.table + place.wk.r * a.table_stride;
+    const size_t head = (size_t)place.wk.h;
+    const int pieces = 16 * n;
+    // page numbers of 32 pieces of 16 tokens (four tiles), two such batches in shared memory and the
+    // next one in a register
+    auto page_of = [&](int sub) {  // sub: piece of 16 tokens, from the unit's first tile
+      const int k0 = s_begin * kKeys + sub * 16;
+      return (unsigned)k0 < (unsigned)held ? table[k0 >> a.page_shift] : -1;
+    };
+    int batch = 0;
+    int ahead = page_of(lane);
+    __syncwarp();
+    sh.pages[w][lane] = ahead;
+    ahead = page_of(32 + lane);
+    __syncwarp();
+    auto issue = [&](int i) {
+      const int p = i >> 3, tile = phase_tile(p, n);
+      const bool is_k = phase_is_k(p, n);
+      if (tile >= 4 * (batch + 1)) {
+        batch++;
+        sh.pages[w][32 * (batch & 1) + lane] = ahead;
+        ahead = page_of(32 * (batch + 1) + lane);
+        __syncwarp();
+      }
+      const int sub = tile * 8 + (i & 7);
+      const int k0 = s_begin * kKeys + sub * 16;
+      const int page = sh.pages[w][sub & 63];
+      const int slot = loads % kRing;
+      const bool there = (unsigned)k0 < (unsigned)held && (unsigned)page < (unsigned)a.n_pages;
+      bad = there ? bad & ~(1u << slot) : bad | (1u << slot);
+      if (lane == 0) {
+        const uint32_t bar = smem_addr(&sh.ring_full[w][slot]);
+        if (there) {
+          const uint8_t* src =
+              a.cache +
+              ((((size_t)page * a.Hkv + head) << (a.page_shift - 4)) + ((k0 & ((1 << a.page_shift) - 1)) >> 4)) *
+                  c4::sub_bytes(D) + (is_k ? 0 : c4::vc_at(D));
+          mbar_arrive_expect_tx(bar, L::piece);
+          bulk_load(ring + slot * L::piece, src, L::piece, bar);
+        } else {
+          mbar_arrive(bar);
+        }
+      }
+      loads++;
+    };
+    int next = w;
+    for (int k = 0; k < kRing && next < pieces; k++, next += kFillWarps) issue(next);
+    for (int i = w; i < pieces; i += kFillWarps) {
+      const int p = i >> 3, s = i & 7, tile = phase_tile(p, n);
+      const bool is_k = phase_is_k(p, n);
+      const int g = tiles_done + tile;               // operand buffer: g & 1, its use g / 2
+      const uint32_t empty = smem_addr(is_k ? &sh.k_empty[g & 1] : &sh.v_empty[g & 1]);
+      ok = mbar_wait(empty, ((g >> 1) & 1) ^ 1, ab);
+      const int slot = used % kRing;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.ring_full[w][slot]), (used / kRing) & 1, ab));
+      if (!ok) break;
+      const uint32_t src = ring + slot * L::piece;
+      const bool none = (bad >> slot) & 1u;
+      const int k0 = (s_begin + tile) * kKeys + s * 16;
+      const uint32_t dst = smem + (is_k ? L::k : L::v) + (g & 1) * L::tile + s * 16 * 128;
+#pragma unroll 1
+      for (int it = 0; it < 2; it++) {
+        const int u = u8 + 8 * it;
+        const uint32_t to = dst + u * 128;
+        if (is_k) {
+          uint32_t x[NG], sc[NG / 2], lo[NG / 2];
+          ld_shared(src + u * 16 * NG + c * 4 * NG, x);
+          ld_shared(src + c4::ks_at(D) + u * 2 * NG, sc);
+          ld_shared(src + c4::km_at(D) + u * 2 * NG, lo);
+#pragma unroll
+          for (int j = 0; j < NG; j++) {
+            const uint32_t pick = (j & 1) ? 0x3232u : 0x1010u;
+            // a page outside the cache: NaN, for every row that sees it
+            const uint32_t scale = none ? 0x7e007e00u : __byte_perm(sc[j / 2], 0, pick);
+            const uint4 v = values8(x[j], scale, __byte_perm(lo[j / 2], 0, pick));
+            st_shared16(to + (j >> 1) * L::half + (((4 * (j & 1) + c) ^ (u & 7)) << 4), v);
+          }
+        } else {
+          const int row = c4::v_row(u);
+          uint32_t x[NG], pair[NG];
+          ld_shared(src + row * 16 * NG + ((2 * c) ^ c4::v_turn(row, NG)) * 2 * NG, x);
+          ld_shared(src + (c4::vp_at(D) - c4::vc_at(D)) + row * 4 * NG, pair);
+          // what lies behind the last key, or was never copied, must not reach the sums: 0 * NaN
+          const bool hide = none || k0 + u >= held;
+#pragma unroll
+          for (int j = 0; j < NG; j++) {
+            const uint32_t word = __byte_perm(x[j / 2], x[NG / 2 + j / 2], (j & 1) ? 0x7632u : 0x5410u);
+            uint4 v = values8(word, __byte_perm(pair[j], 0, 0x1010u), __byte_perm(pair[j], 0, 0x3232u));
+            if (hide) v = make_uint4(0u, 0u, 0u, 0u);
+            st_shared16(to + (j >> 1) * L::half + (((4 * (j & 1) + c) ^ (u & 7)) << 4), v);
+          }
+        }
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(is_k ? &sh.k_full[g & 1] : &sh.v_full[g & 1]));
+      used++;
+      if (next < pieces) issue(next);
+      next += kFillWarps;
+    }
+    tiles_done += n;
+    place.next(a, lane);
+  }
+  // copies in flight land before the CTA exits
+  for (int i = used; i < loads; i++)
+    mbar_wait_drain(smem_addr(&sh.ring_full[w][i % kRing]), (i / kRing) & 1, a.status, kWaitLimitNs);
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_constant__ Cache4AttnArgs a) {
+  using L = Layout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  __shared__ Shared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x;
+  Walk wk;
+  wk.group = a.Hq / a.Hkv;
+  wk.h = 0;
+
+  // ---- this CTA's run of steps, and the unit that it starts in
+  const int per = (a.R + kThreads - 1) / kThreads;
+  const int r_lo = min((int)threadIdx.x * per, a.R), r_hi = min(r_lo + per, a.R);
+  long long mine = 0;
+  for (int r = r_lo; r < r_hi; r++) {
+    wk.request(a, r);
+    mine += (long long)a.Hkv * wk.head_steps();
+  }
+  long long before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += y;
+  }
+  if (lane == 31) sh.scan[warp] = before;
+  const Abort ab{smem_addr(&sh.abort)};
+  if (threadIdx.x == 0) {
+    abort_state_init(sh.abort, a.status, kWaitLimitNs, 0);
+    for (int s = 0; s < 2; s++) {
+      mbar_init(smem_addr(&sh.q_full[s]), 256);
+      mbar_init(smem_addr(&sh.k_full[s]), 8);
+      mbar_init(smem_addr(&sh.v_full[s]), 8);
+      mbar_init(smem_addr(&sh.k_empty[s]), 1);
+      mbar_init(smem_addr(&sh.v_empty[s]), 1);
+      mbar_init(smem_addr(&sh.s_full[s]), 1);
+      mbar_init(smem_addr(&sh.p_full[s]), 256);
+      mbar_init(smem_addr(&sh.o_final[s]), 1);
+    }
+    for (int w = 0; w < kFillWarps; w++)
+      for (int s = 0; s < kRing; s++) mbar_init(smem_addr(&sh.ring_full[w][s]), 1);
+    mbar_init(smem_addr(&sh.drain), 1);
+    fence_barrier_init();
+  }
+  if (warp == 0) tmem_alloc(smem_addr(&sh.tmem), kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  long long total = 0;
+  before -= mine;
+  for (int i = 0; i < kThreads / 32; i++) {
+    if (i < warp) before += sh.scan[i];
+    total += sh.scan[i];
+  }
+  const long long chunk = max((total + gridDim.x - 1) / (long long)gridDim.x, (long long)a.min_chunk);
+  const long long run0 = cta * chunk, run1 = min(run0 + chunk, total);
+  if (run0 < total && before <= run0 && run0 < before + mine) {
+    long long at = before;
+    for (int r = r_lo; r < r_hi; r++) {
+      wk.request(a, r);
+      const long long one = wk.head_steps(), all = one * a.Hkv;
+      if (run0 < at + all) {
+        const int h = (int)((run0 - at) / one);
+        at += h * one;
+        while (run0 >= at + wk.steps()) {
+          at += wk.steps();
+          wk.next_tile();
+        }
+        sh.find_r = r;
+        sh.find_h = h;
+        sh.find_t = wk.t;
+        sh.line0 = at;
+        break;
+      }
+      at += all;
+    }
+  }
+  __syncthreads();
+  long long left = max(0LL, run1 - run0);
+  int s_begin = 0;
+  if (left > 0) {
+    wk.request(a, sh.find_r);
+    wk.h = sh.find_h;
+    while (wk.t < sh.find_t) wk.next_tile();
+    s_begin = (int)(run0 - sh.line0);
+  }
+
+  Place& place = sh.place[warp];
+  if (lane == 0) place = Place{wk, s_begin, left, sh.line0, chunk};
+  __syncwarp();
+
+  if (warp < 4) {
+    if (warp == 0) {
+      // ---------------------------------------------------------------- MMA issuer
+      const uint32_t idesc_qk = idesc_f16_f32(kRows, kKeys, false);
+      const uint32_t idesc_pv = idesc_f16_f32(kRows, D, true);
+      const uint64_t dQ = smem_desc_sw128(smem + L::q, 16, 1024);
+      const uint64_t dK = smem_desc_sw128(smem + L::k, 16, 1024);
+      const uint64_t dV = smem_desc_sw128(smem + L::v, L::half, 1024);
+      constexpr uint32_t kTileDesc = L::tile >> 4;
+      int g = 0, unit = 0, unit_b = 0, gb = 0;   // key tiles and units so far; of tile B
+      bool ok = true;
+      while (place.left > 0 && ok) {
+        const int n = place.steps();
+        const bool two = place.wk.rows() > kRows;
+        ok = mbar_wait(smem_addr(&sh.q_full[0]), unit & 1, ab);
+        if (two && ok) ok = mbar_wait(smem_addr(&sh.q_full[1]), unit_b & 1, ab);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        for (int j = 0; j <= n && ok; j++) {
+          const int gj = g + j, gp = gj - 1;
+          if (j > 0) ok = mbar_wait(smem_addr(&sh.v_full[gp & 1]), (gp >> 1) & 1, ab);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint64_t dKj = dK + (uint64_t)((gj & 1) * kTileDesc), dVj = dV + (uint64_t)((gp & 1) * kTileDesc);
+#pragma unroll
+          for (int t = 0; t < 2; t++) {
+            const uint32_t tS = tmem + t * 128, tO = tmem + 256 + t * D;
+            if (t == 0 || two) {
+              if (j > 0) {
+                const int done = t ? gb + j - 1 : gp;
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.p_full[t]), done & 1, ab));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; kk++)
+                  mma_ts_elect(tO, tS + (kk >> 2) * 64 + (kk & 3) * 8, dVj + (uint64_t)(kk * (2048 >> 4)), idesc_pv,
+                               kk ? 1u : (uint32_t)(j > 1));
+                if (j == n) mma_commit_elect(smem_addr(&sh.o_final[t]));
+              }
+            }
+            if (t == 1 && j > 0) mma_commit_elect(smem_addr(&sh.v_empty[gp & 1]));
+            if ((t == 0 || two) && j < n) {
+              if (t == 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.k_full[gj & 1]), (gj >> 1) & 1, ab));
+                if (!ok) break;
+                tc_fence_after();
+              }
+              const uint64_t dQt = dQ + (uint64_t)(t * kTileDesc);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; kk++) {
+                const uint64_t off = (uint64_t)(((kk >> 2) * L::half + (kk & 3) * 32) >> 4);
+                mma_ss_elect(tS, dQt + off, dKj + off, idesc_qk, kk > 0);
+              }
+              mma_commit_elect(smem_addr(&sh.s_full[t]));
+            }
+          }
+          if (ok && j < n) mma_commit_elect(smem_addr(&sh.k_empty[gj & 1]));
+        }
+        g += n;
+        unit++;
+        if (two) {
+          gb += n;
+          unit_b++;
+        }
+        place.next(a, lane);
+      }
+      mma_commit_elect(smem_addr(&sh.drain));
+      mbar_wait_drain(smem_addr(&sh.drain), 0, a.status, kWaitLimitNs);
+      __syncwarp();
+    } else {
+      fill<D>(a, sh, smem, place, ab);
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax, Q and O
+    const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t bar_id = 1 + t * 4 + quarter;   // the two warps of a row
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + lanes + t * 128 + half * 64;
+    const uint32_t tO = tmem + lanes + 256 + t * D + half * (D / 2);
+    const bool scribe = threadIdx.x == 128;         // writes the CTA's entry of the join list
+    if (scribe) a.joins[2 * cta] = make_int4(0, 0, 0, 0);   // none, so far
+    uint32_t scnt = 0;
+    int unit = 0;
+    while (place.left > 0) {
+      int n, seen;
+      float factor;
+      const bool used = t == 0 || place.wk.rows() > kRows;
+      {
+        const Walk wk = place.wk;
+        const int steps = wk.steps(), s_begin = place.s_begin, rows = wk.rows();
+        n = place.steps();
+        if (scribe && s_begin == 0 && n < steps) {
+          a.joins[2 * cta] = make_int4((int)((place.at + steps - 1) / place.chunk), rows, wk.t, wk.row0);
+          a.joins[2 * cta + 1] = make_int4(wk.h, 0, 0, 0);
+        }
+        if (used) {
+          // ---- Q in fp16, a power of two per row
+          const int full = wk.t * 2 * kRows + t * kRows + row;
+          const bool live = t * kRows + row < rows;
+          const int i = live ? full / wk.group : 0;
+          const int hq = wk.h * wk.group + (live ? full - i * wk.group : 0);
+          constexpr int CH = D / 16;                // 16-byte chunks of the thread's half of the row
+          uint4 x[CH];
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (wk.row0 + i) * a.qs[0] + hq * a.qs[1] +
+                                     half * (D / 2);
+          float big = 0.f;
+#pragma unroll
+          for (int e = 0; e < CH; e++) {
+            x[e] = live ? *reinterpret_cast<const uint4*>(src + 8 * e) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t y[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+#pragma unroll
+            for (int z = 0; z < 4; z++)
+              big = fmax3(big, fabsf(__uint_as_float(y[z] << 16)), fabsf(__uint_as_float(y[z] & 0xffff0000u)));
+          }
+          sh.xq[t][half][row] = big;
+          named_bar_sync(bar_id, 64);
+          big = fmaxf(big, sh.xq[t][half ^ 1][row]);
+          const int ex = max((int)(__float_as_uint(big) >> 23), 9);
+          // the largest channel lands in 2^8 .. 2^9; the scale's sign goes with it
+          float down = __uint_as_float((uint32_t)(262 - ex) << 23);
+          down = a.scale < 0.f ? -down : a.scale == 0.f ? 0.f : down;
+          factor = fmaxf(__uint_as_float((uint32_t)(ex - 8) << 23) * fabsf(a.scale) * 1.4426950408889634f, 1.2e-38f);
+#pragma unroll
+          for (int e = 0; e < CH; e++) {
+            const uint32_t y[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+            float f[8];
+#pragma unroll
+            for (int z = 0; z < 4; z++) {
+              f[2 * z] = __uint_as_float(y[z] << 16) * down;
+              f[2 * z + 1] = __uint_as_float(y[z] & 0xffff0000u) * down;
+            }
+            const int ch = half * CH + e;           // chunk of the row
+            st_shared16(smem + L::q + t * L::tile + (ch >> 3) * L::half + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                        make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]), pack_half2(f[2], f[6]),
+                                   pack_half2(f[3], f[7])));
+          }
+          fence_proxy_async_shared();
+          mbar_arrive(smem_addr(&sh.q_full[t]));
+          // keys that the row sees, counted from this thread's first score
+          seen = (live ? max(0, wk.held - (wk.n - 1 - i)) : wk.sees()) - s_begin * kKeys - half * 64;
+        }
+      }
+      if (used) {
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < n; j++, scnt++, seen -= kKeys) {
+          ok = mbar_wait(smem_addr(&sh.s_full[t]), scnt & 1, ab);
+          __syncwarp();
+          ok = __all_sync(0xffffffffu, ok);
+          tc_fence_after();
+          const bool cut = __any_sync(0xffffffffu, seen < 64);
+          float mraw = -INFINITY, rs = 0.f, alpha = 1.f;
+          bool rescale = false, stored = false;
+          if (ok) {
+            uint32_t x0[32], x1[32];
+            load_s64(tS, cut, seen, x0, x1);
+            mraw = max64(x0, x1);
+            // the common case: every row of the warp has a maximum, and none exceeds it by too much
+            if (__all_sync(0xffffffffu, m > -INFINITY && mraw * factor <= m + kGrow)) {
+              rs = write_p64(x0, x1, factor, -m, tS);
+              stored = true;
+            }
+          }
+          if (named_bar_or(bar_id, 64, !stored || !ok)) {
+            sh.xmax[scnt & 1][t][half][row] = mraw;
+            ok = named_bar_and(bar_id, 64, ok);
+            if (!ok) break;
+            const float mt = fmaxf(mraw, sh.xmax[scnt & 1][t][half ^ 1][row]) * factor;
+            const float mnew = mt > m + kGrow ? ceilf(mt) - kBelow : m;
+            alpha = mnew == m ? 1.f : exp2_int(m - mnew);   // (-inf - -inf)
+            rescale = j > 0 && mnew != m;
+            if (!stored) {
+              uint32_t x0[32], x1[32];
+              load_s64(tS, cut, seen, x0, x1);
+              // a row that has seen no key yet: its scores are all -inf
+              rs = write_p64(x0, x1, factor, mnew == -INFINITY ? 0.f : -mnew, tS);
+            } else if (__any_sync(0xffffffffu, mnew != m)) {
+              scale_p64(tS, alpha);
+              rs *= alpha;
+            }
+            m = mnew;
+          }
+          l = l * alpha + rs;
+          // PV of the previous tile has completed (S of this one landed after it)
+          if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+            for (int ch = 0; ch < D / 32; ch++) {
+              uint32_t o[16];
+              tmem_ld16(tO + ch * 16, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 16; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+              tmem_st16(tO + ch * 16, o);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(smem_addr(&sh.p_full[t]));
+        }
+        if (ok) {
+          ok = mbar_wait(smem_addr(&sh.o_final[t]), unit & 1, ab);
+          __syncwarp();
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        unit++;
+        if (half == 1) sh.xsum[t][row] = l;
+        named_bar_sync(bar_id, 64);
+        if (half == 0) sh.xsum[t][row] += l;
+        ok = named_bar_and(bar_id, 64, ok);
+        const float lsum = sh.xsum[t][row];
+        if (!ok) break;
+        tc_fence_after();
+
+        // ---- O, or this CTA's part of it
+        const Walk wk = place.wk;
+        const bool starts = place.s_begin == 0, whole = starts && n == wk.steps();
+        const int full = wk.t * 2 * kRows + t * kRows + row;
+        const bool live = t * kRows + row < wk.rows();
+        const int i = live ? full / wk.group : 0;
+        const int hq = wk.h * wk.group + (live ? full - i * wk.group : 0);
+        const float inv = whole ? 1.f / lsum : 1.f;
+        const int part = 2 * cta + (starts ? 1 : 0);
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + ((size_t)(wk.row0 + i) * a.Hq + hq) * D + half * (D / 2);
+        float* dst_part = a.part_o + ((size_t)part * 2 * kRows + t * kRows + row) * D + half * (D / 2);
+#pragma unroll
+        for (int ch = 0; ch < D / 32; ch++) {
+          uint32_t o[16];
+          tmem_ld16(tO + ch * 16, o);
+          tmem_wait_ld();
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 2; e++) {           // eight channels, in the order 0 4 1 5 2 6 3 7
+              float f[8];
+#pragma unroll
+              for (int z = 0; z < 8; z++)
+                f[z] = lsum == 0.f ? 0.f : __uint_as_float(o[8 * e + (z & 3) * 2 + (z >> 2)]) * inv;
+              if (whole) {
+                *reinterpret_cast<uint4*>(dst + ch * 16 + 8 * e) =
+                    make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                               pack_bf16x2(f[6], f[7]));
+              } else {
+                *reinterpret_cast<float4*>(dst_part + ch * 16 + 8 * e) = make_float4(f[0], f[1], f[2], f[3]);
+                *reinterpret_cast<float4*>(dst_part + ch * 16 + 8 * e + 4) = make_float4(f[4], f[5], f[6], f[7]);
+              }
+            }
+          }
+        }
+        if (live && half == 0) {
+          if (whole) {
+            if (a.lse)
+              a.lse[(size_t)hq * a.T + wk.row0 + i] =
+                  lsum == 0.f ? -INFINITY : (m + log2f(lsum)) * 0.6931471805599453f;
+          } else {
+            float* ml = a.part_ml + (size_t)part * 4 * kRows + t * kRows + row;
+            ml[0] = m;
+            ml[2 * kRows] = lsum;
+          }
+        }
+      }
+      place.next(a, lane);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the parts of the tile that CTA blockIdx.x of the first launch started and did not end.
+// Eight threads a row, 32 rows a block.
+template <int D>
+__global__ void __launch_bounds__(256) cache4_tc_join_kernel(const __grid_constant__ Cache4AttnArgs a) {
+  const int first = blockIdx.x;
+  const int4 j0 = a.joins[2 * first], j1 = a.joins[2 * first + 1];
+  const int last = j0.x, rows = j0.y, group = a.Hq / a.Hkv;
+  const int row = blockIdx.y * 32 + (threadIdx.x >> 3), col = (threadIdx.x & 7) * (D / 8);
+  if (row >= rows) return;  // no tile: rows is 0
+  const int full = j0.z * 2 * kRows + row, i = full / group, hq = j1.x * group + full - i * group;
+  float M = -INFINITY, Ls = 0.f;
+  for (int p = first; p <= last; p++) {
+    const float* ml = a.part_ml + (size_t)(2 * p + (p == first)) * 4 * kRows + row;
+    M = fmaxf(M, ml[0]);
+  }
+  const float top = M == -INFINITY ? 0.f : M;
+  float sum[D / 8] = {};
+#pragma unroll 2
+  for (int p = first; p <= last; p++) {
+    const int id = 2 * p + (p == first);
+    const float* ml = a.part_ml + (size_t)id * 4 * kRows + row;
+    const float f = ex2(ml[0] - top);
+    Ls = fmaf(ml[2 * kRows], f, Ls);
+    const float4* src = reinterpret_cast<const float4*>(a.part_o + ((size_t)id * 2 * kRows + row) * D + col);
+#pragma unroll
+    for (int e = 0; e < D / 32; e++) {
+      const float4 y = src[e];
+      sum[4 * e] = fmaf(y.x, f, sum[4 * e]);
+      sum[4 * e + 1] = fmaf(y.y, f, sum[4 * e + 1]);
+      sum[4 * e + 2] = fmaf(y.z, f, sum[4 * e + 2]);
+      sum[4 * e + 3] = fmaf(y.w, f, sum[4 * e + 3]);
+    }
+  }
+  const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) +
+                                              ((size_t)(j0.w + i) * a.Hq + hq) * D + col);
+#pragma unroll
+  for (int e = 0; e < D / 16; e++) dst[e] = pack_bf16x2(sum[2 * e] * inv, sum[2 * e + 1] * inv);
+  if (a.lse && col == 0)
+    a.lse[(size_t)hq * a.T + j0.w + i] = Ls == 0.f ? -INFINITY : (top + log2f(Ls)) * 0.6931471805599453f;
+}
+
+template <int D>
+cudaError_t go(Cache4AttnArgs a, cudaStream_t st) {
+  auto kernel = cache4_tc_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::bytes);
+  if (e != cudaSuccess) return e;
+  kernel<<<kCache4TcCtas, kThreads, Layout<D>::bytes, st>>>(a);
+  if ((e = cudaGetLastError())) return e;
+  cache4_tc_join_kernel<D><<<dim3(kCache4TcCtas, 2 * kRows / 32), 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache4_tc(Cache4AttnArgs a, cudaStream_t st) {
+  a.min_chunk = 4;
+  return a.d == 64 ? go<64>(a, st) : go<128>(a, st);
+}
+
+}  // namespace s2

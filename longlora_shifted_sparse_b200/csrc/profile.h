@@ -24,6 +24,7 @@ enum KernelId {
   kCache4Append,
   kCache4Read,
   kCache4Attn,
+  kCache4Tc,
   kCache4AttnSimt,
   kNumKernels
 };
@@ -31,7 +32,7 @@ enum KernelId {
 inline const char* const kKernelNames[kNumKernels] = {
     "rope_table", "rope_pi", "fwd_tc", "fwd_simt", "bwd_rowsum", "bwd_dkdv_tc", "bwd_dq_tc",
     "bwd_dq_simt", "bwd_dkdv_simt", "rope", "page_plan", "cache4_append", "cache4_read",
-    "cache4_attn", "cache4_attn_simt"};
+    "cache4_attn", "cache4_tc", "cache4_attn_simt"};
 
 struct Record {
   int id;

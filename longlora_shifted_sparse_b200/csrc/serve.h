@@ -65,16 +65,21 @@ struct Cache4AttnArgs {
   long long qs[2], table_stride;
   int R, T, Hq, Hkv, d, page_shift, n_pages, max_pages, max_new;
   float scale;
-  // the tensor-core kernel's workspace: arrival counters (zero between calls), and two parts a
-  // CTA: output sums, then maxima and sums of the rows
+  // workspace: the status word (a bounded wait expired), arrival counters (zero between calls), the
+  // list of tiles to join, and two parts a CTA: output sums, then maxima and sums of the rows
+  unsigned* status;
   unsigned* counters;
+  int4* joins;
   float* part_o;
   float* part_ml;
-  int min_chunk;      // steps of 32 keys that a CTA takes at least
+  int min_chunk;      // steps that a CTA takes at least
 };
+// few rows: bf16, d = 64, 128 or 256
 constexpr int kCache4MaxCtas = 148 * 4, kCache4PartRows = 32, kCache4PartFloats = 4096;
-// bf16, d = 64, 128 or 256
 cudaError_t launch_cache4_attn(Cache4AttnArgs a, cudaStream_t st);
+// many rows: bf16, d = 64 or 128
+constexpr int kCache4TcCtas = 148, kCache4TcRows = 256;
+cudaError_t launch_cache4_tc(Cache4AttnArgs a, cudaStream_t st);
 // any type and head dim
 cudaError_t launch_cache4_attn_simt(const Cache4AttnArgs& a, bool bf16, cudaStream_t st);
 

@@ -35,11 +35,23 @@ bool cache_ok(int n_pages, int page_size) {
   return n_pages > 0 && (long long)n_pages * page_size <= 0x7fffffffLL;
 }
 
-// The attention's workspace: the arrival counters, then the parts.
-constexpr size_t kCounterBytes = (kCache4MaxCtas * sizeof(unsigned) + 255) / 256 * 256;
+// The attention's workspace: the status word, the arrival counters, the list of joins, and the
+// parts of whichever kernel runs.
+constexpr size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+constexpr size_t kAtCounters = 256;
+constexpr size_t kAtJoins = kAtCounters + round256(kCache4MaxCtas * sizeof(unsigned));
+constexpr size_t kAtParts = kAtJoins + round256(kCache4TcCtas * 2 * sizeof(int4));
+constexpr size_t kPartsO = (size_t)2 * kCache4MaxCtas * kCache4PartFloats;
+constexpr size_t kTcPartsO = (size_t)2 * kCache4TcCtas * kCache4TcRows * 128;
+constexpr size_t kPartsFloats = kPartsO + (size_t)2 * kCache4MaxCtas * 2 * kCache4PartRows;
+constexpr size_t kTcPartsFloats = kTcPartsO + (size_t)2 * kCache4TcCtas * 2 * kCache4TcRows;
+constexpr size_t kCache4WsBytes =
+    kAtParts + sizeof(float) * (kPartsFloats > kTcPartsFloats ? kPartsFloats : kTcPartsFloats);
 
-// Tensor-core kernel: bf16 and a head dim that is a whole number of its wide loads.
-bool cache4_tc(int d, int dt) { return dt == S2_BF16 && (d == 64 || d == 128 || d == 256); }
+// Tensor instructions: bf16 and a head dim that is a whole number of their wide loads.
+bool cache4_mma(int d, int dt) { return dt == S2_BF16 && (d == 64 || d == 128 || d == 256); }
+// Many rows of a kv head: tiles of 256 rows rather than of 8 to 32.
+bool cache4_many(int d, long long rows) { return (d == 64 || d == 128) && rows > 64; }
 
 }  // namespace
 }  // namespace s2
@@ -190,7 +202,7 @@ s2_status s2attn_cache4_read(const void* cache, const int* slots, void* k, void*
 }
 
 size_t s2attn_cache4_workspace_bytes(void) {
-  return kCounterBytes + (size_t)2 * kCache4MaxCtas * (kCache4PartFloats + 2 * kCache4PartRows) * sizeof(float);
+  return kCache4WsBytes;
 }
 
 s2_status s2attn_cache4_attn(const void* q, const void* cache, const int* block_table,
@@ -208,7 +220,7 @@ s2_status s2attn_cache4_attn(const void* q, const void* cache, const int* block_
   if (!headdim32_ok(d)) return S2_ERR_HEADDIM;
   const int shift = page_shift(page_size);
   if (shift < 0 || !isfinite(scale)) return S2_ERR_ARG;
-  if ((long long)max_pages << shift > 0x7fffffffLL) return S2_ERR_SHAPE;
+  if ((long long)max_pages << shift > 0x7fffff00LL) return S2_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(cache) || !aligned16(o) || !strides16(q_strides, 2, dtype))
     return S2_ERR_ALIGN;
   if (!workspace || ws_bytes < s2attn_cache4_workspace_bytes()) return S2_ERR_WORKSPACE;
@@ -221,10 +233,17 @@ s2_status s2attn_cache4_attn(const void* q, const void* cache, const int* block_
   a.n_pages = n_pages; a.max_pages = max_pages; a.max_new = max_new; a.scale = scale;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool bf16 = dtype == S2_BF16;
-  if (cache4_tc(d, dtype)) {
-    a.counters = static_cast<unsigned*>(workspace);
-    a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
-    a.part_ml = a.part_o + (size_t)2 * kCache4MaxCtas * kCache4PartFloats;
+  if (cache4_mma(d, dtype)) {
+    char* ws = static_cast<char*>(workspace);
+    a.status = reinterpret_cast<unsigned*>(ws);
+    a.counters = reinterpret_cast<unsigned*>(ws + kAtCounters);
+    a.joins = reinterpret_cast<int4*>(ws + kAtJoins);
+    a.part_o = reinterpret_cast<float*>(ws + kAtParts);
+    if (cache4_many(d, (long long)max_new * (H_q / H_kv))) {
+      a.part_ml = a.part_o + kTcPartsO;
+      return to_status(timed_launch(kCache4Tc, s, [&] { return launch_cache4_tc(a, s); }));
+    }
+    a.part_ml = a.part_o + kPartsO;
     return to_status(timed_launch(kCache4Attn, s, [&] { return launch_cache4_attn(a, s); }));
   }
   return to_status(timed_launch(kCache4AttnSimt, s, [&] { return launch_cache4_attn_simt(a, bf16, s); }));
