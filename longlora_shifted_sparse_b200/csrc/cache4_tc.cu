@@ -6,23 +6,23 @@
 // dequantised key and value. Bound by the tensor cores and, at their speed, by the softmax and
 // the dequantisation beside them; the cache's own bytes are read once per 256 rows.
 //
-// Roles (640 threads, 96 registers each):
+// Roles (512 threads, 128 registers each):
 //   warp 0        MMA issuer and TMEM owner. Per tile of 128 keys: PV_A(j-1), QK_A(j), PV_B(j-1),
 //                 QK_B(j), so that one tile's softmax runs under the other's MMAs.
-//   warps 1..3    copies and dequantisation. Sixteen tokens' k (or v) are one contiguous piece of
+//   warps 1..7    copies and dequantisation. Sixteen tokens' k (or v) are one contiguous piece of
 //                 10 d bytes, fetched by a bulk copy into the warp's ring of kRing; then
 //                 minimum + scale * code in fp16 is written as the MMAs' 128-byte-swizzled operands (K
 //                 rows of channels; V the same, read by the MMA transposed). K runs one tile
 //                 ahead of V, as their buffers come free. Channels lie in the order 0 4 1 5 2 6 3 7
 //                 within each eight, the order in which two codes come out of a word together:
-//                 Q is written in the same order, and O is put right when it is stored.
-//   warps 4..19   softmax: a row (TMEM lane) is shared by two warps, 64 of the 128 scores each.
-//                 They also bring Q to fp16 (a power of two per row makes it fit, and returns in
-//                 the scores' factor) and store O.
+//                 Q, which they bring to fp16 too, is written in the same order, and O is put right
+//                 when it is stored.
+//   warps 8..15   softmax and O, a thread a row (TMEM lane).
 // fp16 holds k and v to half a step 2^-12 of the value (the codes are 4 bits wide) and P to 2^-12
 // of itself; scores, maxima, sums and O are fp32.
-// The running maximum is kept as an integer 4 below the row's (P then uses fp16's range) and moves
-// only when a score exceeds it by 12, so that O is rescaled, exactly, a few times a row.
+// The running maximum is kept as an integer 4 below the row's first ones (P then uses fp16's range)
+// and moves only when a sum of P shows that some P might leave that range, so that the common
+// step takes no maximum and O is rescaled, exactly, a few times a row.
 //
 // Work is steps of 128 keys, laid on one line over (request, kv head, tile) with the steps that the
 // tile's last row sees; every CTA takes an equal run of the line. A tile that several CTAs share
@@ -40,10 +40,11 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kRows = 128, kKeys = 128, kThreads = 640;
-constexpr int kFillWarps = 3, kRing = 6;      // pieces in flight of each dequantising warp
+constexpr int kFillWarps = 7, kRing = 3;      // pieces in flight of each dequantising warp
+constexpr int kRows = 128, kKeys = 128, kThreads = 32 * (1 + kFillWarps + 8);
 constexpr uint32_t kTmemCols = 512;
-constexpr float kBelow = 4.f, kGrow = 12.f;   // log2 units
+constexpr float kBelow = 4.f, kGrow = 5.f;    // log2 units
+constexpr float kSumLimit = 60000.f;          // no P of such a sum overflows fp16
 
 template <int D>
 struct Layout {
@@ -130,17 +131,17 @@ struct Place {
 };
 
 struct Shared {
-  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2], o_final[2], drain;
   uint64_t ring_full[kFillWarps][kRing];
   AbortState abort;
   uint32_t tmem;
-  float xmax[2][2][2][kRows], xq[2][2][kRows], xsum[2][kRows];
+  float factor[2][2][kRows];   // scores' factor of each row, of even and odd units of a tile
   int pages[kFillWarps][64];
   Place place[kThreads / 32];
   long long scan[kThreads / 32];
-  long long line0;           // where the found unit begins on the line
-  int find_r, find_h, find_t, found;
+  Walk found;                // the unit that the run begins in, and its place on the line
+  long long line0;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -151,16 +152,6 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 // 1024 + code, and 64 + code, of a word's codes 0 and 4, and 1 and 5, in fp16.
@@ -174,14 +165,19 @@ __device__ __forceinline__ uint32_t codes15(uint32_t x) {
   asm("lop3.b32 %0, %1, 0x00f000f0, %2, 0xea;" : "=r"(r) : "r"(x), "r"(0x54005400u));
   return r;
 }
-// Eight values of a word, in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ uint4 values8(uint32_t x, uint32_t scale, uint32_t low) {
-  const uint32_t y = x >> 8;
-  return make_uint4(hfma2(hsub2(codes04(x), 0x64006400u), scale, low),
-                    hfma2(hsub2(codes15(x), 0x54005400u), scale, low),
-                    hfma2(hsub2(codes04(y), 0x64006400u), scale, low),
-                    hfma2(hsub2(codes15(y), 0x54005400u), scale, low));
+__device__ __forceinline__ uint32_t value2(uint32_t code, uint32_t offset, __half2 scale, __half2 low) {
+  const __half2 c = __hsub2(*reinterpret_cast<__half2*>(&code), *reinterpret_cast<__half2*>(&offset));
+  const __half2 v = __hfma2(c, scale, low);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
+// Eight values of a word, in the order 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ uint4 values8(uint32_t x, __half2 scale, __half2 low) {
+  const uint32_t y = x >> 8;
+  return make_uint4(value2(codes04(x), 0x64006400u, scale, low), value2(codes15(x), 0x54005400u, scale, low),
+                    value2(codes04(y), 0x64006400u, scale, low), value2(codes15(y), 0x54005400u, scale, low));
+}
+__device__ __forceinline__ __half2 twice_lo(uint32_t x) { return __low2half2(*reinterpret_cast<__half2*>(&x)); }
+__device__ __forceinline__ __half2 twice_hi(uint32_t x) { return __high2half2(*reinterpret_cast<__half2*>(&x)); }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -210,82 +206,96 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_maj
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Max of a thread's 64 scores, as a tree of three-input maxima.
-__device__ __forceinline__ float max64(const uint32_t (&x0)[32], const uint32_t (&x1)[32]) {
-  float v[64];
-#pragma unroll
-  for (int c = 0; c < 32; c++) {
-    v[c] = __uint_as_float(x0[c]);
-    v[32 + c] = __uint_as_float(x1[c]);
-  }
-  float m1[22];
-#pragma unroll
-  for (int c = 0; c < 21; c++) m1[c] = fmax3(v[3 * c], v[3 * c + 1], v[3 * c + 2]);
-  m1[21] = v[63];
-  float m2[8];
-#pragma unroll
-  for (int c = 0; c < 7; c++) m2[c] = fmax3(m1[3 * c], m1[3 * c + 1], m1[3 * c + 2]);
-  m2[7] = m1[21];
-  return fmax3(fmax3(m2[0], m2[1], m2[2]), fmax3(m2[3], m2[4], m2[5]), fmaxf(m2[6], m2[7]));
-}
+// ------------------------------------------------------------------ softmax
 
-// P = exp2(S * factor + shift) for 64 scores, as fp16 pairs over the first 32 of their columns of
-// S; returns the sum of P.
-__device__ __forceinline__ float write_p64(const uint32_t (&x0)[32], const uint32_t (&x1)[32], float factor,
-                                           float shift, uint32_t tS) {
+// Waits for this thread's TMEM loads; x, one of their destinations, is not read before.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&x)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]),
+                 "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]),
+                 "+r"(x[15]), "+r"(x[16]), "+r"(x[17]), "+r"(x[18]), "+r"(x[19]), "+r"(x[20]), "+r"(x[21]),
+                 "+r"(x[22]), "+r"(x[23]), "+r"(x[24]), "+r"(x[25]), "+r"(x[26]), "+r"(x[27]), "+r"(x[28]),
+                 "+r"(x[29]), "+r"(x[30]), "+r"(x[31])
+               :
+               : "memory");
+}
+// 32 scores of a row; those of keys from `seen` on (counted from the first) become -inf.
+__device__ __forceinline__ void hide32(bool cut, int seen, uint32_t (&x)[32]) {
+  if (cut)
+#pragma unroll
+    for (int c = 0; c < 32; c++) x[c] = c < seen ? x[c] : 0xff800000u;
+}
+// P = exp2(S * factor + shift) of 32 scores as 16 fp16 pairs; their sum is added to acc.
+__device__ __forceinline__ void p32(const uint32_t (&x)[32], float factor, float shift, uint32_t* pk, uint64_t& acc) {
   const uint64_t f2 = f2pack(factor, factor), s2 = f2pack(shift, shift);
-  uint64_t acc = f2pack(0.f, 0.f);
 #pragma unroll
-  for (int ch = 0; ch < 2; ch++) {
-    uint32_t pk[16];
-#pragma unroll
-    for (int c = 0; c < 16; c++) {
-      const float u0 = __uint_as_float(ch ? x1[2 * c] : x0[2 * c]);
-      const float u1 = __uint_as_float(ch ? x1[2 * c + 1] : x0[2 * c + 1]);
-      float a0, a1;
-      f2unpack(ffma2(f2pack(u0, u1), f2, s2), a0, a1);
-      const float p0 = ex2(a0), p1 = ex2(a1);
-      acc = fadd2(acc, f2pack(p0, p1));
-      pk[c] = pack_half2(p0, p1);
-    }
-    tmem_st16(tS + ch * 16, pk);
+  for (int c = 0; c < 16; c++) {
+    float a0, a1;
+    f2unpack(ffma2(f2pack(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), f2, s2), a0, a1);
+    const float p0 = ex2(a0), p1 = ex2(a1);
+    acc = fadd2(acc, f2pack(p0, p1));
+    pk[c] = pack_half2(p0, p1);
   }
+}
+__device__ __forceinline__ float both(uint64_t acc) {
   float r0, r1;
   f2unpack(acc, r0, r1);
   return r0 + r1;
 }
-
-// Brings the 64 P that a thread wrote to a maximum that moved, by an exact power of two.
-__device__ __forceinline__ void scale_p64(uint32_t tS, float f) {
+// Brings 64 P that were written to a maximum that moved, by an exact power of two.
+__device__ __forceinline__ void scale_p64(uint32_t tP, float f) {
   uint32_t x[32];
-  tmem_ld32(tS, x);
-  tmem_wait_ld();
+  tmem_ld32(tP, x);
+  tmem_wait_ld32(x);
 #pragma unroll
   for (int c = 0; c < 32; c++) {
     const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[c]));
     x[c] = pack_half2(y.x * f, y.y * f);
   }
-  tmem_st32(tS, x);
+  tmem_st32(tP, x);
 }
-
 // 2^k for an integral k <= 0 (k = -inf gives 0), exact.
 __device__ __forceinline__ float exp2_int(float k) {
   return k < -126.f ? 0.f : __int_as_float((static_cast<int>(k) + 127) << 23);
 }
 
-// A thread's 64 scores; those of keys from `seen` on (counted from its first) become -inf.
-__device__ __forceinline__ void load_s64(uint32_t tS, bool cut, int seen, uint32_t (&x0)[32], uint32_t (&x1)[32]) {
-  tmem_ld32(tS, x0);
-  tmem_ld32(tS + 32, x1);
-  tmem_wait_ld();
-  if (cut) {
-    const uint32_t ninf = 0xff800000u;
+// The row's P where the running maximum m does not serve: none yet, or scores far above it. The
+// first `done` of the two halves of 64 have their P already (sum rs). Takes the maximum of the others,
+// moves m to an integer kBelow under it, and writes P. Returns what the older sums have to be
+// multiplied by. Warp-collective; out of the common path, it reads S twice.
+__device__ __forceinline__ float p_anew(uint32_t tS, int done, bool cut, int seen, float factor, float& m, float& rs) {
+  float top = -INFINITY;
+  for (int c = 2 * done; c < 4; c++) {
+    uint32_t x[32];
+    tmem_ld32(tS + c * 32, x);
+    tmem_wait_ld32(x);
+    hide32(cut, seen - c * 32, x);
 #pragma unroll
-    for (int c = 0; c < 32; c++) {
-      x0[c] = c < seen ? x0[c] : ninf;
-      x1[c] = 32 + c < seen ? x1[c] : ninf;
-    }
+    for (int e = 0; e < 32; e += 2) top = fmax3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
   }
+  top *= factor;
+  const float mnew = top > m + kGrow ? ceilf(top) - kBelow : m;
+  const float alpha = mnew == m ? 1.f : exp2_int(m - mnew);   // (-inf - -inf)
+  if (done == 1) {
+    scale_p64(tS, alpha);
+    rs *= alpha;
+  }
+  uint64_t acc = f2pack(0.f, 0.f);
+  for (int h = done; h < 2; h++) {
+    uint32_t x[32], pk[32];
+#pragma unroll
+    for (int c = 0; c < 2; c++) {
+      tmem_ld32(tS + h * 64 + c * 32, x);
+      tmem_wait_ld32(x);
+      hide32(cut, seen - h * 64 - c * 32, x);
+      // a row that has seen no key yet: its scores are all -inf
+      p32(x, factor, mnew == -INFINITY ? 0.f : -mnew, pk + 16 * c, acc);
+    }
+    tmem_st32(tS + h * 64, pk);
+  }
+  rs += both(acc);
+  m = mnew;
+  return alpha;
 }
 
 // ------------------------------------------------------------------ copies and dequantisation
@@ -296,6 +306,58 @@ __device__ __forceinline__ bool phase_is_k(int p, int n) { return p == 0 || ((p 
 __device__ __forceinline__ int phase_tile(int p, int n) {
   return p == 0 ? 0 : p == 2 * n - 1 ? n - 1 : (p & 1) ? (p + 1) / 2 : p / 2 - 1;
 }
+
+// Query rows of a tile of 128 in fp16. A power of two a row brings its largest channel to 2^8 .. 2^9
+// (bf16's bits then fit, but for what is below 2^-29 of that channel); it returns in the scores'
+// factor. The scale's sign goes with the row.
+template <int D>
+struct QueryRows {
+  static constexpr int kLanes = D / 8, kPerWarp = 32 / kLanes;                      // lanes a row, rows a warp
+  static constexpr int kMine = (kRows + kFillWarps * kPerWarp - 1) / (kFillWarps * kPerWarp);  // rows a lane
+  uint4 x[kMine];
+  __device__ __forceinline__ int row(int b) const {
+    return (b * kFillWarps + (threadIdx.x >> 5) - 1) * kPerWarp + (threadIdx.x & 31) / kLanes;
+  }
+  __device__ __forceinline__ void load(const Cache4AttnArgs& a, const Walk& wk, int t) {
+    const int ch = threadIdx.x % kLanes, rows = min(kRows, wk.rows() - t * kRows);
+#pragma unroll
+    for (int b = 0; b < kMine; b++) {
+      x[b] = make_uint4(0u, 0u, 0u, 0u);
+      if (row(b) < rows) {
+        const int full = wk.t * 2 * kRows + t * kRows + row(b), i = full / wk.group;
+        x[b] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (wk.row0 + i) * a.qs[0] +
+                                               (wk.h * wk.group + full - i * wk.group) * a.qs[1] + 8 * ch);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(const Cache4AttnArgs& a, uint32_t dst, float* factor) const {
+    const int ch = threadIdx.x % kLanes;
+#pragma unroll
+    for (int b = 0; b < kMine; b++) {
+      const int r = row(b);
+      const uint32_t y[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
+      float f[8], big = 0.f;
+#pragma unroll
+      for (int z = 0; z < 4; z++) {
+        f[2 * z] = __uint_as_float(y[z] << 16);
+        f[2 * z + 1] = __uint_as_float(y[z] & 0xffff0000u);
+        big = fmax3(big, fabsf(f[2 * z]), fabsf(f[2 * z + 1]));
+      }
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      const int ex = max((int)(__float_as_uint(big) >> 23), 9);
+      float down = __uint_as_float((uint32_t)(262 - ex) << 23);
+      down = a.scale < 0.f ? -down : a.scale == 0.f ? 0.f : down;
+      if (r < kRows) {
+        st_shared16(dst + (ch >> 3) * Layout<D>::half + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                    make_uint4(pack_half2(f[0] * down, f[4] * down), pack_half2(f[1] * down, f[5] * down),
+                               pack_half2(f[2] * down, f[6] * down), pack_half2(f[3] * down, f[7] * down)));
+        if (ch == 0)  // never 0: a hidden score times it stays -inf
+          factor[r] = fmaxf(__uint_as_float((uint32_t)(ex - 8) << 23) * fabsf(a.scale) * 1.4426950408889634f, 1.2e-38f);
+      }
+    }
+  }
+};
 
 template <int D>
 __device__ __forceinline__ void fill(const Cache4AttnArgs& a, Shared& sh, uint32_t smem, Place& place,
@@ -308,12 +370,12 @@ __device__ __forceinline__ void fill(const Cache4AttnArgs& a, Shared& sh, uint32
   int loads = 0, used = 0;       // pieces copied and consumed by this warp, over all units
   uint32_t bad = 0;              // a bit a ring slot: nothing was copied (a page outside the cache)
   int tiles_done = 0;            // tiles of earlier units
+  int units[2] = {0, 0};         // units so far that use tile A, tile B
   bool ok = true;
   while (place.left > 0 && ok) {
     const int s_begin = place.s_begin, n = place.steps(), held = place.wk.held;
     const int* table = a.table + place.wk.r * a.table_stride;
     const size_t head = (size_t)place.wk.h;
-    const int pieces = 16 * n;
     // page numbers of 32 pieces of 16 tokens (four tiles), two such batches in shared memory and the
     // next one in a register
     auto page_of = [&](int sub) {  // sub: piece of 16 tokens, from the unit's first tile
@@ -326,16 +388,17 @@ __device__ __forceinline__ void fill(const Cache4AttnArgs& a, Shared& sh, uint32
     sh.pages[w][lane] = ahead;
     ahead = page_of(32 + lane);
     __syncwarp();
-    auto issue = [&](int i) {
-      const int p = i >> 3, tile = phase_tile(p, n);
-      const bool is_k = phase_is_k(p, n);
+    int ip = 0, is = w;            // phase and piece that is copied next
+    auto issue = [&]() {
+      if (ip >= 2 * n) return;
+      const int tile = phase_tile(ip, n);
       if (tile >= 4 * (batch + 1)) {
         batch++;
         sh.pages[w][32 * (batch & 1) + lane] = ahead;
         ahead = page_of(32 * (batch + 1) + lane);
         __syncwarp();
       }
-      const int sub = tile * 8 + (i & 7);
+      const int sub = tile * 8 + is;
       const int k0 = s_begin * kKeys + sub * 16;
       const int page = sh.pages[w][sub & 63];
       const int slot = loads % kRing;
@@ -347,7 +410,7 @@ __device__ __forceinline__ void fill(const Cache4AttnArgs& a, Shared& sh, uint32
           const uint8_t* src =
               a.cache +
               ((((size_t)page * a.Hkv + head) << (a.page_shift - 4)) + ((k0 & ((1 << a.page_shift) - 1)) >> 4)) *
-                  c4::sub_bytes(D) + (is_k ? 0 : c4::vc_at(D));
+                  c4::sub_bytes(D) + (phase_is_k(ip, n) ? 0 : c4::vc_at(D));
           mbar_arrive_expect_tx(bar, L::piece);
           bulk_load(ring + slot * L::piece, src, L::piece, bar);
         } else {
@@ -355,63 +418,98 @@ __device__ __forceinline__ void fill(const Cache4AttnArgs& a, Shared& sh, uint32
         }
       }
       loads++;
+      is += kFillWarps;
+      if (is >= 8) {
+        is -= 8;
+        ip++;
+      }
     };
-    int next = w;
-    for (int k = 0; k < kRing && next < pieces; k++, next += kFillWarps) issue(next);
-    for (int i = w; i < pieces; i += kFillWarps) {
-      const int p = i >> 3, s = i & 7, tile = phase_tile(p, n);
+    for (int k = 0; k < kRing; k++) issue();
+    bool queries = true;           // still to be brought in: after the first keys
+    for (int p = 0, s = w; p < 2 * n;) {
+      if (p > 0 && queries) {
+        queries = false;
+        const Walk wk = place.wk;
+        for (int t = 0; t < 2 && ok; t++) {
+          if (t == 1 && wk.rows() <= kRows) break;
+          QueryRows<D> qr;
+          qr.load(a, wk, t);
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.q_empty[t]), (units[t] & 1) ^ 1, ab));
+          if (!ok) break;
+          qr.store(a, smem + L::q + t * L::tile, sh.factor[units[t] & 1][t]);
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh.q_full[t]));
+          units[t]++;
+        }
+        if (!ok) break;
+      }
+      const int tile = phase_tile(p, n);
       const bool is_k = phase_is_k(p, n);
       const int g = tiles_done + tile;               // operand buffer: g & 1, its use g / 2
       const uint32_t empty = smem_addr(is_k ? &sh.k_empty[g & 1] : &sh.v_empty[g & 1]);
-      ok = mbar_wait(empty, ((g >> 1) & 1) ^ 1, ab);
       const int slot = used % kRing;
+      ok = mbar_wait(empty, ((g >> 1) & 1) ^ 1, ab) &&
+           mbar_wait(smem_addr(&sh.ring_full[w][slot]), (used / kRing) & 1, ab);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.ring_full[w][slot]), (used / kRing) & 1, ab));
       if (!ok) break;
       const uint32_t src = ring + slot * L::piece;
       const bool none = (bad >> slot) & 1u;
       const int k0 = (s_begin + tile) * kKeys + s * 16;
       const uint32_t dst = smem + (is_k ? L::k : L::v) + (g & 1) * L::tile + s * 16 * 128;
-#pragma unroll 1
-      for (int it = 0; it < 2; it++) {
-        const int u = u8 + 8 * it;
-        const uint32_t to = dst + u * 128;
-        if (is_k) {
-          uint32_t x[NG], sc[NG / 2], lo[NG / 2];
-          ld_shared(src + u * 16 * NG + c * 4 * NG, x);
-          ld_shared(src + c4::ks_at(D) + u * 2 * NG, sc);
-          ld_shared(src + c4::km_at(D) + u * 2 * NG, lo);
+      if (is_k) {
+        uint32_t x[2][NG], sc[2][NG / 2], lo[2][NG / 2];
 #pragma unroll
-          for (int j = 0; j < NG; j++) {
-            const uint32_t pick = (j & 1) ? 0x3232u : 0x1010u;
-            // a page outside the cache: NaN, for every row that sees it
-            const uint32_t scale = none ? 0x7e007e00u : __byte_perm(sc[j / 2], 0, pick);
-            const uint4 v = values8(x[j], scale, __byte_perm(lo[j / 2], 0, pick));
-            st_shared16(to + (j >> 1) * L::half + (((4 * (j & 1) + c) ^ (u & 7)) << 4), v);
-          }
-        } else {
-          const int row = c4::v_row(u);
-          uint32_t x[NG], pair[NG];
-          ld_shared(src + row * 16 * NG + ((2 * c) ^ c4::v_turn(row, NG)) * 2 * NG, x);
-          ld_shared(src + (c4::vp_at(D) - c4::vc_at(D)) + row * 4 * NG, pair);
-          // what lies behind the last key, or was never copied, must not reach the sums: 0 * NaN
-          const bool hide = none || k0 + u >= held;
+        for (int it = 0; it < 2; it++) {
+          const int u = u8 + 8 * it;
+          ld_shared(src + u * 16 * NG + c * 4 * NG, x[it]);
+          ld_shared(src + c4::ks_at(D) + u * 2 * NG, sc[it]);
+          ld_shared(src + c4::km_at(D) + u * 2 * NG, lo[it]);
+          // a page outside the cache: NaN, for every row that sees it
+          if (none)
 #pragma unroll
-          for (int j = 0; j < NG; j++) {
-            const uint32_t word = __byte_perm(x[j / 2], x[NG / 2 + j / 2], (j & 1) ? 0x7632u : 0x5410u);
-            uint4 v = values8(word, __byte_perm(pair[j], 0, 0x1010u), __byte_perm(pair[j], 0, 0x3232u));
-            if (hide) v = make_uint4(0u, 0u, 0u, 0u);
-            st_shared16(to + (j >> 1) * L::half + (((4 * (j & 1) + c) ^ (u & 7)) << 4), v);
-          }
+            for (int j = 0; j < NG / 2; j++) sc[it][j] = 0x7e007e00u;
         }
+#pragma unroll
+        for (int j = 0; j < NG; j++)
+#pragma unroll
+          for (int it = 0; it < 2; it++) {
+            const uint32_t s2 = sc[it][j / 2], l2 = lo[it][j / 2];
+            st_shared16(dst + (u8 + 8 * it) * 128 + (j >> 1) * L::half + (((4 * (j & 1) + c) ^ u8) << 4),
+                        (j & 1) ? values8(x[it][j], twice_hi(s2), twice_hi(l2))
+                                : values8(x[it][j], twice_lo(s2), twice_lo(l2)));
+          }
+      } else {
+        uint32_t x[2][NG], pair[2][NG];
+        bool hide[2];
+#pragma unroll
+        for (int it = 0; it < 2; it++) {
+          const int u = u8 + 8 * it, row = c4::v_row(u);
+          ld_shared(src + row * 16 * NG + ((2 * c) ^ c4::v_turn(row, NG)) * 2 * NG, x[it]);
+          ld_shared(src + (c4::vp_at(D) - c4::vc_at(D)) + row * 4 * NG, pair[it]);
+          // what lies behind the last key, or was never copied, must not reach the sums: 0 * NaN
+          hide[it] = none || (unsigned)(k0 + u) >= (unsigned)held;
+        }
+#pragma unroll
+        for (int j = 0; j < NG; j++)
+#pragma unroll
+          for (int it = 0; it < 2; it++) {
+            const uint32_t word = __byte_perm(x[it][j / 2], x[it][NG / 2 + j / 2], (j & 1) ? 0x7632u : 0x5410u);
+            const uint32_t pr = hide[it] ? 0u : pair[it][j];
+            st_shared16(dst + (u8 + 8 * it) * 128 + (j >> 1) * L::half + (((4 * (j & 1) + c) ^ u8) << 4),
+                        values8(word, twice_lo(pr), twice_hi(pr)));
+          }
       }
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(is_k ? &sh.k_full[g & 1] : &sh.v_full[g & 1]));
       used++;
-      if (next < pieces) issue(next);
-      next += kFillWarps;
+      issue();
+      s += kFillWarps;
+      if (s >= 8) {
+        s -= 8;
+        p++;
+      }
     }
     tiles_done += n;
     place.next(a, lane);
@@ -454,13 +552,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
   if (threadIdx.x == 0) {
     abort_state_init(sh.abort, a.status, kWaitLimitNs, 0);
     for (int s = 0; s < 2; s++) {
-      mbar_init(smem_addr(&sh.q_full[s]), 256);
+      mbar_init(smem_addr(&sh.q_full[s]), kFillWarps);
+      // the last QK^T has read Q, and each softmax warp its factors
+      mbar_init(smem_addr(&sh.q_empty[s]), 1 + 4);
       mbar_init(smem_addr(&sh.k_full[s]), 8);
       mbar_init(smem_addr(&sh.v_full[s]), 8);
       mbar_init(smem_addr(&sh.k_empty[s]), 1);
       mbar_init(smem_addr(&sh.v_empty[s]), 1);
       mbar_init(smem_addr(&sh.s_full[s]), 1);
-      mbar_init(smem_addr(&sh.p_full[s]), 256);
+      mbar_init(smem_addr(&sh.p_full[s]), kRows);
       mbar_init(smem_addr(&sh.o_final[s]), 1);
     }
     for (int w = 0; w < kFillWarps; w++)
@@ -493,9 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
           at += wk.steps();
           wk.next_tile();
         }
-        sh.find_r = r;
-        sh.find_h = h;
-        sh.find_t = wk.t;
+        wk.h = h;
+        sh.found = wk;
         sh.line0 = at;
         break;
       }
@@ -506,9 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
   long long left = max(0LL, run1 - run0);
   int s_begin = 0;
   if (left > 0) {
-    wk.request(a, sh.find_r);
-    wk.h = sh.find_h;
-    while (wk.t < sh.find_t) wk.next_tile();
+    wk = sh.found;
     s_begin = (int)(run0 - sh.line0);
   }
 
@@ -516,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
   if (lane == 0) place = Place{wk, s_begin, left, sh.line0, chunk};
   __syncwarp();
 
-  if (warp < 4) {
+  if (warp <= kFillWarps) {
     if (warp == 0) {
       // ---------------------------------------------------------------- MMA issuer
       const uint32_t idesc_qk = idesc_f16_f32(kRows, kKeys, false);
@@ -525,63 +622,68 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
       const uint64_t dK = smem_desc_sw128(smem + L::k, 16, 1024);
       const uint64_t dV = smem_desc_sw128(smem + L::v, L::half, 1024);
       constexpr uint32_t kTileDesc = L::tile >> 4;
-      int g = 0, unit = 0, unit_b = 0, gb = 0;   // key tiles and units so far; of tile B
+      // Steps run on across units: a unit's last PVs go out in the next one's first step, so that
+      // its softmax and its output run under the next one's first MMAs.
+      int g = 0;                              // key tiles so far
+      int units0 = 0, units1 = 0, p0 = 0, p1 = 0;   // units and p_full phases so far, of tile A and B
+      int n = 0, j = 0;                       // steps of the unit, and the next one
+      bool two = false, pv = false, pv_two = false, pv_on = false, pv_last = false;  // pv: of the last step
       bool ok = true;
-      while (place.left > 0 && ok) {
-        const int n = place.steps();
-        const bool two = place.wk.rows() > kRows;
-        ok = mbar_wait(smem_addr(&sh.q_full[0]), unit & 1, ab);
-        if (two && ok) ok = mbar_wait(smem_addr(&sh.q_full[1]), unit_b & 1, ab);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        for (int j = 0; j <= n && ok; j++) {
-          const int gj = g + j, gp = gj - 1;
-          if (j > 0) ok = mbar_wait(smem_addr(&sh.v_full[gp & 1]), (gp >> 1) & 1, ab);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const uint64_t dKj = dK + (uint64_t)((gj & 1) * kTileDesc), dVj = dV + (uint64_t)((gp & 1) * kTileDesc);
+      while (true) {
+        const bool flush = place.left <= 0;
+        if (flush && !pv) break;
+        if (!flush && j == 0) {
+          n = place.steps();
+          two = place.wk.rows() > kRows;
+        }
+        const int gp = g - 1;
+        if (pv) ok = mbar_wait(smem_addr(&sh.v_full[gp & 1]), (gp >> 1) & 1, ab);
+        const uint64_t dKj = dK + (uint64_t)((g & 1) * kTileDesc), dVj = dV + (uint64_t)((gp & 1) * kTileDesc);
 #pragma unroll
-          for (int t = 0; t < 2; t++) {
-            const uint32_t tS = tmem + t * 128, tO = tmem + 256 + t * D;
-            if (t == 0 || two) {
-              if (j > 0) {
-                const int done = t ? gb + j - 1 : gp;
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.p_full[t]), done & 1, ab));
-                if (!ok) break;
-                tc_fence_after();
+        for (int t = 0; t < 2; t++) {
+          const uint32_t tS = tmem + t * 128, tO = tmem + 256 + t * D;
+          if (pv && (t == 0 || pv_two)) {
+            ok = ok && mbar_wait(smem_addr(&sh.p_full[t]), (t ? p1++ : p0++) & 1, ab);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; kk++)
-                  mma_ts_elect(tO, tS + (kk >> 2) * 64 + (kk & 3) * 8, dVj + (uint64_t)(kk * (2048 >> 4)), idesc_pv,
-                               kk ? 1u : (uint32_t)(j > 1));
-                if (j == n) mma_commit_elect(smem_addr(&sh.o_final[t]));
-              }
+            for (int kk = 0; kk < kKeys / 16; kk++)
+              mma_ts_elect(tO, tS + (kk >> 2) * 64 + (kk & 3) * 8, dVj + (uint64_t)(kk * (2048 >> 4)), idesc_pv,
+                           kk ? 1u : (uint32_t)pv_on);
+            if (pv_last) mma_commit_elect(smem_addr(&sh.o_final[t]));
+          }
+          if (t == 1 && pv) mma_commit_elect(smem_addr(&sh.v_empty[gp & 1]));
+          if (!flush && (t == 0 || two)) {
+            if (j == 0) ok = ok && mbar_wait(smem_addr(&sh.q_full[t]), (t ? units1 : units0) & 1, ab);
+            if (t == 0) ok = ok && mbar_wait(smem_addr(&sh.k_full[g & 1]), (g >> 1) & 1, ab);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dQt = dQ + (uint64_t)(t * kTileDesc);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; kk++) {
+              const uint64_t off = (uint64_t)(((kk >> 2) * L::half + (kk & 3) * 32) >> 4);
+              mma_ss_elect(tS, dQt + off, dKj + off, idesc_qk, kk > 0);
             }
-            if (t == 1 && j > 0) mma_commit_elect(smem_addr(&sh.v_empty[gp & 1]));
-            if ((t == 0 || two) && j < n) {
-              if (t == 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.k_full[gj & 1]), (gj >> 1) & 1, ab));
-                if (!ok) break;
-                tc_fence_after();
-              }
-              const uint64_t dQt = dQ + (uint64_t)(t * kTileDesc);
-#pragma unroll
-              for (int kk = 0; kk < D / 16; kk++) {
-                const uint64_t off = (uint64_t)(((kk >> 2) * L::half + (kk & 3) * 32) >> 4);
-                mma_ss_elect(tS, dQt + off, dKj + off, idesc_qk, kk > 0);
-              }
-              mma_commit_elect(smem_addr(&sh.s_full[t]));
+            mma_commit_elect(smem_addr(&sh.s_full[t]));
+            if (j == n - 1) {
+              mma_commit_elect(smem_addr(&sh.q_empty[t]));
+              t ? units1++ : units0++;
             }
           }
-          if (ok && j < n) mma_commit_elect(smem_addr(&sh.k_empty[gj & 1]));
         }
-        g += n;
-        unit++;
-        if (two) {
-          gb += n;
-          unit_b++;
+        if (!ok || flush) break;
+        mma_commit_elect(smem_addr(&sh.k_empty[g & 1]));
+        pv = true;
+        pv_two = two;
+        pv_on = j > 0;
+        pv_last = j == n - 1;
+        g++;
+        if (++j == n) {
+          j = 0;
+          place.next(a, lane);
         }
-        place.next(a, lane);
       }
       mma_commit_elect(smem_addr(&sh.drain));
       mbar_wait_drain(smem_addr(&sh.drain), 0, a.status, kWaitLimitNs);
@@ -590,20 +692,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
       fill<D>(a, sh, smem, place, ab);
     }
   } else {
-    // ------------------------------------------------------------------ softmax, Q and O
-    const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quarter = warp & 3;
+    // ------------------------------------------------------------------ softmax and O
+    const int t = (warp - kFillWarps - 1) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    const uint32_t bar_id = 1 + t * 4 + quarter;   // the two warps of a row
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t tS = tmem + lanes + t * 128 + half * 64;
-    const uint32_t tO = tmem + lanes + 256 + t * D + half * (D / 2);
-    const bool scribe = threadIdx.x == 128;         // writes the CTA's entry of the join list
+    const uint32_t tS = tmem + lanes + t * 128, tO = tmem + lanes + 256 + t * D;
+    const bool scribe = threadIdx.x == 32 * (1 + kFillWarps);   // writes the CTA's entry of the join list
     if (scribe) a.joins[2 * cta] = make_int4(0, 0, 0, 0);   // none, so far
     uint32_t scnt = 0;
     int unit = 0;
     while (place.left > 0) {
-      int n, seen;
-      float factor;
+      int n, seen = 0;
       const bool used = t == 0 || place.wk.rows() > kRows;
       {
         const Walk wk = place.wk;
@@ -613,122 +712,72 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
           a.joins[2 * cta] = make_int4((int)((place.at + steps - 1) / place.chunk), rows, wk.t, wk.row0);
           a.joins[2 * cta + 1] = make_int4(wk.h, 0, 0, 0);
         }
-        if (used) {
-          // ---- Q in fp16, a power of two per row
-          const int full = wk.t * 2 * kRows + t * kRows + row;
-          const bool live = t * kRows + row < rows;
-          const int i = live ? full / wk.group : 0;
-          const int hq = wk.h * wk.group + (live ? full - i * wk.group : 0);
-          constexpr int CH = D / 16;                // 16-byte chunks of the thread's half of the row
-          uint4 x[CH];
-          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (wk.row0 + i) * a.qs[0] + hq * a.qs[1] +
-                                     half * (D / 2);
-          float big = 0.f;
-#pragma unroll
-          for (int e = 0; e < CH; e++) {
-            x[e] = live ? *reinterpret_cast<const uint4*>(src + 8 * e) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t y[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
-#pragma unroll
-            for (int z = 0; z < 4; z++)
-              big = fmax3(big, fabsf(__uint_as_float(y[z] << 16)), fabsf(__uint_as_float(y[z] & 0xffff0000u)));
-          }
-          sh.xq[t][half][row] = big;
-          named_bar_sync(bar_id, 64);
-          big = fmaxf(big, sh.xq[t][half ^ 1][row]);
-          const int ex = max((int)(__float_as_uint(big) >> 23), 9);
-          // the largest channel lands in 2^8 .. 2^9; the scale's sign goes with it
-          float down = __uint_as_float((uint32_t)(262 - ex) << 23);
-          down = a.scale < 0.f ? -down : a.scale == 0.f ? 0.f : down;
-          factor = fmaxf(__uint_as_float((uint32_t)(ex - 8) << 23) * fabsf(a.scale) * 1.4426950408889634f, 1.2e-38f);
-#pragma unroll
-          for (int e = 0; e < CH; e++) {
-            const uint32_t y[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
-            float f[8];
-#pragma unroll
-            for (int z = 0; z < 4; z++) {
-              f[2 * z] = __uint_as_float(y[z] << 16) * down;
-              f[2 * z + 1] = __uint_as_float(y[z] & 0xffff0000u) * down;
-            }
-            const int ch = half * CH + e;           // chunk of the row
-            st_shared16(smem + L::q + t * L::tile + (ch >> 3) * L::half + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
-                        make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]), pack_half2(f[2], f[6]),
-                                   pack_half2(f[3], f[7])));
-          }
-          fence_proxy_async_shared();
-          mbar_arrive(smem_addr(&sh.q_full[t]));
-          // keys that the row sees, counted from this thread's first score
-          seen = (live ? max(0, wk.held - (wk.n - 1 - i)) : wk.sees()) - s_begin * kKeys - half * 64;
-        }
+        const int full = wk.t * 2 * kRows + t * kRows + row;
+        const bool live = t * kRows + row < rows;
+        // keys that the row sees, counted from the unit's first
+        seen = (live ? max(0, wk.held - (wk.n - 1 - full / wk.group)) : wk.sees()) - s_begin * kKeys;
       }
       if (used) {
         float m = -INFINITY, l = 0.f;
-        bool ok = true;
+        bool ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.q_full[t]), unit & 1, ab));
+        if (!ok) break;
+        const float factor = sh.factor[unit & 1][t][row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.q_empty[t]));
         for (int j = 0; j < n; j++, scnt++, seen -= kKeys) {
-          ok = mbar_wait(smem_addr(&sh.s_full[t]), scnt & 1, ab);
-          __syncwarp();
-          ok = __all_sync(0xffffffffu, ok);
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.s_full[t]), scnt & 1, ab));
+          if (!ok) break;
           tc_fence_after();
-          const bool cut = __any_sync(0xffffffffu, seen < 64);
-          float mraw = -INFINITY, rs = 0.f, alpha = 1.f;
-          bool rescale = false, stored = false;
-          if (ok) {
-            uint32_t x0[32], x1[32];
-            load_s64(tS, cut, seen, x0, x1);
-            mraw = max64(x0, x1);
-            // the common case: every row of the warp has a maximum, and none exceeds it by too much
-            if (__all_sync(0xffffffffu, m > -INFINITY && mraw * factor <= m + kGrow)) {
-              rs = write_p64(x0, x1, factor, -m, tS);
-              stored = true;
+          const bool cut = __any_sync(0xffffffffu, seen < kKeys);
+          float rs = 0.f, alpha = 1.f;
+          // The common case: every row of the warp has a maximum m, and P with it does not overflow,
+          // which the sum of P shows: no maximum is taken. P goes over the first 32 columns of its half of S.
+          int done = 0;
+          if (__all_sync(0xffffffffu, m > -INFINITY)) {
+            uint32_t x[2][32], pk[32];
+            tmem_ld32(tS, x[0]);
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              uint64_t acc = f2pack(0.f, 0.f);
+#pragma unroll
+              for (int c = 0; c < 2; c++) {
+                tmem_wait_ld32(x[c]);
+                if (2 * h + c < 3) tmem_ld32(tS + (2 * h + c + 1) * 32, x[c ^ 1]);
+                hide32(cut, seen - (2 * h + c) * 32, x[c]);
+                p32(x[c], factor, -m, pk + 16 * c, acc);
+              }
+              const float sum = both(acc);
+              if (done != h || !__all_sync(0xffffffffu, sum <= kSumLimit)) continue;
+              tmem_st32(tS + h * 64, pk);
+              rs += sum;
+              done++;
             }
           }
-          if (named_bar_or(bar_id, 64, !stored || !ok)) {
-            sh.xmax[scnt & 1][t][half][row] = mraw;
-            ok = named_bar_and(bar_id, 64, ok);
-            if (!ok) break;
-            const float mt = fmaxf(mraw, sh.xmax[scnt & 1][t][half ^ 1][row]) * factor;
-            const float mnew = mt > m + kGrow ? ceilf(mt) - kBelow : m;
-            alpha = mnew == m ? 1.f : exp2_int(m - mnew);   // (-inf - -inf)
-            rescale = j > 0 && mnew != m;
-            if (!stored) {
-              uint32_t x0[32], x1[32];
-              load_s64(tS, cut, seen, x0, x1);
-              // a row that has seen no key yet: its scores are all -inf
-              rs = write_p64(x0, x1, factor, mnew == -INFINITY ? 0.f : -mnew, tS);
-            } else if (__any_sync(0xffffffffu, mnew != m)) {
-              scale_p64(tS, alpha);
-              rs *= alpha;
+          if (done < 2) {
+            tmem_wait_st();
+            const float was = m;
+            alpha = p_anew(tS, done, cut, seen, factor, m, rs);
+            // PV of the previous tile has completed (S of this one landed after it)
+            if (j > 0 && __any_sync(0xffffffffu, m != was)) {
+#pragma unroll 1
+              for (int ch = 0; ch < D / 32; ch++) {
+                uint32_t o[32];
+                tmem_ld32(tO + ch * 32, o);
+                tmem_wait_ld32(o);
+#pragma unroll
+                for (int c = 0; c < 32; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                tmem_st32(tO + ch * 32, o);
+              }
             }
-            m = mnew;
           }
           l = l * alpha + rs;
-          // PV of the previous tile has completed (S of this one landed after it)
-          if (__any_sync(0xffffffffu, rescale)) {
-#pragma unroll
-            for (int ch = 0; ch < D / 32; ch++) {
-              uint32_t o[16];
-              tmem_ld16(tO + ch * 16, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int c = 0; c < 16; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-              tmem_st16(tO + ch * 16, o);
-            }
-          }
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(smem_addr(&sh.p_full[t]));
         }
-        if (ok) {
-          ok = mbar_wait(smem_addr(&sh.o_final[t]), unit & 1, ab);
-          __syncwarp();
-          ok = __all_sync(0xffffffffu, ok);
-        }
+        ok = ok && mbar_wait(smem_addr(&sh.o_final[t]), unit & 1, ab);
         unit++;
-        if (half == 1) sh.xsum[t][row] = l;
-        named_bar_sync(bar_id, 64);
-        if (half == 0) sh.xsum[t][row] += l;
-        ok = named_bar_and(bar_id, 64, ok);
-        const float lsum = sh.xsum[t][row];
-        if (!ok) break;
+        if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
 
         // ---- O, or this CTA's part of it
@@ -738,42 +787,41 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
         const bool live = t * kRows + row < wk.rows();
         const int i = live ? full / wk.group : 0;
         const int hq = wk.h * wk.group + (live ? full - i * wk.group : 0);
-        const float inv = whole ? 1.f / lsum : 1.f;
+        const float inv = l == 0.f ? 0.f : whole ? 1.f / l : 1.f;
         const int part = 2 * cta + (starts ? 1 : 0);
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + ((size_t)(wk.row0 + i) * a.Hq + hq) * D + half * (D / 2);
-        float* dst_part = a.part_o + ((size_t)part * 2 * kRows + t * kRows + row) * D + half * (D / 2);
-#pragma unroll
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + ((size_t)(wk.row0 + i) * a.Hq + hq) * D;
+        float* dst_part = a.part_o + ((size_t)part * 2 * kRows + t * kRows + row) * D;
+#pragma unroll 1
         for (int ch = 0; ch < D / 32; ch++) {
-          uint32_t o[16];
-          tmem_ld16(tO + ch * 16, o);
-          tmem_wait_ld();
+          uint32_t o[32];
+          tmem_ld32(tO + ch * 32, o);
+          tmem_wait_ld32(o);
           if (live) {
 #pragma unroll
-            for (int e = 0; e < 2; e++) {           // eight channels, in the order 0 4 1 5 2 6 3 7
+            for (int e = 0; e < 4; e++) {           // eight channels, in the order 0 4 1 5 2 6 3 7
               float f[8];
 #pragma unroll
-              for (int z = 0; z < 8; z++)
-                f[z] = lsum == 0.f ? 0.f : __uint_as_float(o[8 * e + (z & 3) * 2 + (z >> 2)]) * inv;
+              for (int z = 0; z < 8; z++) f[z] = __uint_as_float(o[8 * e + (z & 3) * 2 + (z >> 2)]) * inv;
               if (whole) {
-                *reinterpret_cast<uint4*>(dst + ch * 16 + 8 * e) =
+                *reinterpret_cast<uint4*>(dst + ch * 32 + 8 * e) =
                     make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                                pack_bf16x2(f[6], f[7]));
               } else {
-                *reinterpret_cast<float4*>(dst_part + ch * 16 + 8 * e) = make_float4(f[0], f[1], f[2], f[3]);
-                *reinterpret_cast<float4*>(dst_part + ch * 16 + 8 * e + 4) = make_float4(f[4], f[5], f[6], f[7]);
+                *reinterpret_cast<float4*>(dst_part + ch * 32 + 8 * e) = make_float4(f[0], f[1], f[2], f[3]);
+                *reinterpret_cast<float4*>(dst_part + ch * 32 + 8 * e + 4) = make_float4(f[4], f[5], f[6], f[7]);
               }
             }
           }
         }
-        if (live && half == 0) {
+        tc_fence_before();
+        if (live) {
           if (whole) {
             if (a.lse)
-              a.lse[(size_t)hq * a.T + wk.row0 + i] =
-                  lsum == 0.f ? -INFINITY : (m + log2f(lsum)) * 0.6931471805599453f;
+              a.lse[(size_t)hq * a.T + wk.row0 + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
           } else {
             float* ml = a.part_ml + (size_t)part * 4 * kRows + t * kRows + row;
             ml[0] = m;
-            ml[2 * kRows] = lsum;
+            ml[2 * kRows] = l;
           }
         }
       }
@@ -796,7 +844,7 @@ __global__ void __launch_bounds__(256) cache4_tc_join_kernel(const __grid_consta
   const int first = blockIdx.x;
   const int4 j0 = a.joins[2 * first], j1 = a.joins[2 * first + 1];
   const int last = j0.x, rows = j0.y, group = a.Hq / a.Hkv;
-  const int row = blockIdx.y * 32 + (threadIdx.x >> 3), col = (threadIdx.x & 7) * (D / 8);
+  const int row = blockIdx.y * 32 + (threadIdx.x >> 3), col = (threadIdx.x & 7) * 4;  // and every 32 more
   if (row >= rows) return;  // no tile: rows is 0
   const int full = j0.z * 2 * kRows + row, i = full / group, hq = j1.x * group + full - i * group;
   float M = -INFINITY, Ls = 0.f;
@@ -815,7 +863,7 @@ __global__ void __launch_bounds__(256) cache4_tc_join_kernel(const __grid_consta
     const float4* src = reinterpret_cast<const float4*>(a.part_o + ((size_t)id * 2 * kRows + row) * D + col);
 #pragma unroll
     for (int e = 0; e < D / 32; e++) {
-      const float4 y = src[e];
+      const float4 y = src[8 * e];
       sum[4 * e] = fmaf(y.x, f, sum[4 * e]);
       sum[4 * e + 1] = fmaf(y.y, f, sum[4 * e + 1]);
       sum[4 * e + 2] = fmaf(y.z, f, sum[4 * e + 2]);
@@ -823,10 +871,11 @@ __global__ void __launch_bounds__(256) cache4_tc_join_kernel(const __grid_consta
     }
   }
   const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) +
-                                              ((size_t)(j0.w + i) * a.Hq + hq) * D + col);
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + ((size_t)(j0.w + i) * a.Hq + hq) * D + col;
 #pragma unroll
-  for (int e = 0; e < D / 16; e++) dst[e] = pack_bf16x2(sum[2 * e] * inv, sum[2 * e + 1] * inv);
+  for (int e = 0; e < D / 32; e++)
+    *reinterpret_cast<uint2*>(dst + 32 * e) =
+        make_uint2(pack_bf16x2(sum[4 * e] * inv, sum[4 * e + 1] * inv), pack_bf16x2(sum[4 * e + 2] * inv, sum[4 * e + 3] * inv));
   if (a.lse && col == 0)
     a.lse[(size_t)hq * a.T + j0.w + i] = Ls == 0.f ? -INFINITY : (top + log2f(Ls)) * 0.6931471805599453f;
 }
