@@ -10,7 +10,7 @@
 //   warp 0        MMA issuer and TMEM owner. Per tile of 128 keys: PV_A(j-1), QK_A(j), PV_B(j-1),
 //                 QK_B(j), so that one tile's softmax runs under the other's MMAs.
 //   warps 1..7    copies and dequantisation. Sixteen tokens' k (or v) are one contiguous piece of
-//                 10 d bytes, fetched by a bulk copy into the warp's ring of kRing; then
+//                 10 d bytes, fetched a tile ahead by asynchronous copies; then
 //                 minimum + scale * code in fp16 is written as the MMAs' 128-byte-swizzled operands (K
 //                 rows of channels; V the same, read by the MMA transposed). K runs one tile
 //                 ahead of V, as their buffers come free. Channels lie in the order 0 4 1 5 2 6 3 7
@@ -40,8 +40,12 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kFillWarps = 7, kRing = 3;      // pieces in flight of each dequantising warp
-constexpr int kRows = 128, kKeys = 128, kThreads = 32 * (1 + kFillWarps + 8);
+constexpr int kRows = 128, kKeys = 128;
+// Warps: the issuer and three idle ones, eight that fill, eight of the softmax. Five share one
+// scheduler's registers, so a launch hands each thread 96; then they are split (setmaxnreg).
+constexpr int kFill0 = 4, kFillWarps = 8, kSoft0 = 12, kThreads = 640;
+constexpr int kRegsIssue = 40, kRegsFill = 80, kRegsSoftmax = 136;
+static_assert(kRegsIssue + 2 * kRegsFill + 2 * kRegsSoftmax <= 5 * 96, "register split exceeds the launch allocation");
 constexpr uint32_t kTmemCols = 512;
 constexpr float kBelow = 4.f, kGrow = 5.f;    // log2 units
 constexpr float kSumLimit = 60000.f;          // no P of such a sum overflows fp16
@@ -52,7 +56,7 @@ struct Layout {
   static constexpr uint32_t half = kKeys * 128;         // its first 64 channels
   static constexpr uint32_t piece = 10 * D;             // 16 tokens of k, or of v
   static constexpr uint32_t q = 0, k = 2 * tile, v = 4 * tile, ring = 6 * tile;
-  static constexpr uint32_t bytes = ring + kFillWarps * kRing * piece + 1024;
+  static constexpr uint32_t bytes = ring + 2 * kFillWarps * piece + 1024;
 };
 
 // The line of work: requests in order; in a request kv heads, then tiles of 256 rows, then steps.
@@ -131,13 +135,11 @@ struct Place {
 };
 
 struct Shared {
-  uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t q_full[2], q_empty[2], kv_full[2], kv_empty[2];
   uint64_t s_full[2], p_full[2], o_final[2], drain;
-  uint64_t ring_full[kFillWarps][kRing];
   AbortState abort;
   uint32_t tmem;
   float factor[2][2][kRows];   // scores' factor of each row, of even and odd units of a tile
-  int pages[kFillWarps][64];
   Place place[kThreads / 32];
   long long scan[kThreads / 32];
   Walk found;                // the unit that the run begins in, and its place on the line
@@ -178,12 +180,11 @@ __device__ __forceinline__ uint4 values8(uint32_t x, __half2 scale, __half2 low)
 }
 __device__ __forceinline__ __half2 twice_lo(uint32_t x) { return __low2half2(*reinterpret_cast<__half2*>(&x)); }
 __device__ __forceinline__ __half2 twice_hi(uint32_t x) { return __high2half2(*reinterpret_cast<__half2*>(&x)); }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void st_shared16(uint32_t at, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
@@ -300,12 +301,14 @@ __device__ __forceinline__ float p_anew(uint32_t tS, int done, bool cut, int see
 
 // ------------------------------------------------------------------ copies and dequantisation
 
-// Pieces of a unit of n tiles: phase 0 is K_0, then K_1, V_0, K_2, V_1 .. K_{n-1}, V_{n-2}, V_{n-1};
-// eight pieces a phase, dealt to the warps in turn.
-__device__ __forceinline__ bool phase_is_k(int p, int n) { return p == 0 || ((p & 1) && p != 2 * n - 1); }
-__device__ __forceinline__ int phase_tile(int p, int n) {
-  return p == 0 ? 0 : p == 2 * n - 1 ? n - 1 : (p & 1) ? (p + 1) / 2 : p / 2 - 1;
-}
+// What a dequantising warp needs of a tile of 128 keys: its own sixteen tokens, and at a unit's first
+// tile the unit's rows.
+struct Tile {
+  const uint8_t* src;     // their sub-block; null: nothing is copied (no key, or a page outside the cache)
+  int keys;               // how many of them are keys of the request
+  bool first;
+  int row0, h, t, rows;
+};
 
 // Query rows of a tile of 128 in fp16. A power of two a row brings its largest channel to 2^8 .. 2^9
 // (bf16's bits then fit, but for what is below 2^-29 of that channel); it returns in the scores'
@@ -316,17 +319,17 @@ struct QueryRows {
   static constexpr int kMine = (kRows + kFillWarps * kPerWarp - 1) / (kFillWarps * kPerWarp);  // rows a lane
   uint4 x[kMine];
   __device__ __forceinline__ int row(int b) const {
-    return (b * kFillWarps + (threadIdx.x >> 5) - 1) * kPerWarp + (threadIdx.x & 31) / kLanes;
+    return (b * kFillWarps + (threadIdx.x >> 5) - kFill0) * kPerWarp + (threadIdx.x & 31) / kLanes;
   }
-  __device__ __forceinline__ void load(const Cache4AttnArgs& a, const Walk& wk, int t) {
-    const int ch = threadIdx.x % kLanes, rows = min(kRows, wk.rows() - t * kRows);
+  __device__ __forceinline__ void load(const Cache4AttnArgs& a, const Tile& u, int t) {
+    const int ch = threadIdx.x % kLanes, rows = min(kRows, u.rows - t * kRows), group = a.Hq / a.Hkv;
 #pragma unroll
     for (int b = 0; b < kMine; b++) {
       x[b] = make_uint4(0u, 0u, 0u, 0u);
       if (row(b) < rows) {
-        const int full = wk.t * 2 * kRows + t * kRows + row(b), i = full / wk.group;
-        x[b] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (wk.row0 + i) * a.qs[0] +
-                                               (wk.h * wk.group + full - i * wk.group) * a.qs[1] + 8 * ch);
+        const int full = u.t * 2 * kRows + t * kRows + row(b), i = full / group;
+        x[b] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (u.row0 + i) * a.qs[0] +
+                                               (u.h * group + full - i * group) * a.qs[1] + 8 * ch);
       }
     }
   }
@@ -359,164 +362,142 @@ struct QueryRows {
   }
 };
 
+// Warp w takes tokens 16 w .. 16 w + 15 of every tile of the run. Phase g writes K of tile g and V of
+// tile g - 1: those buffers come free, and are needed, together.
 template <int D>
 __device__ __forceinline__ void fill(const Cache4AttnArgs& a, Shared& sh, uint32_t smem, Place& place,
                                      const Abort ab) {
   using L = Layout<D>;
   constexpr int NG = D / 32;
-  const int w = (threadIdx.x >> 5) - 1, lane = threadIdx.x & 31;
-  const int c = lane & 3, u8 = ((lane >> 2) & 1) * 4 + (lane >> 3);
-  const uint32_t ring = smem + L::ring + w * kRing * L::piece;
-  int loads = 0, used = 0;       // pieces copied and consumed by this warp, over all units
-  uint32_t bad = 0;              // a bit a ring slot: nothing was copied (a page outside the cache)
-  int tiles_done = 0;            // tiles of earlier units
-  int units[2] = {0, 0};         // units so far that use tile A, tile B
-  bool ok = true;
-  while (place.left > 0 && ok) {
-    const int s_begin = place.s_begin, n = place.steps(), held = place.wk.held;
-    const int* table = a.table + place.wk.r * a.table_stride;
-    const size_t head = (size_t)place.wk.h;
-    // page numbers of 32 pieces of 16 tokens (four tiles), two such batches in shared memory and the
-    // next one in a register
-    auto page_of = [&](int sub) {  // sub: piece of 16 tokens, from the unit's first tile
-      const int k0 = s_begin * kKeys + sub * 16;
-      return (unsigned)k0 < (unsigned)held ? table[k0 >> a.page_shift] : -1;
-    };
-    int batch = 0;
-    int ahead = page_of(lane);
+  const int w = (threadIdx.x >> 5) - kFill0, lane = threadIdx.x & 31;
+  const int c = lane & 3, u8 = ((lane >> 2) & 1) * 4 + (lane >> 3), v8 = c4::v_row(u8);
+  const uint32_t raw_k = smem + L::ring + w * 2 * L::piece, raw_v = raw_k + L::piece;
+  // where this lane's 16-byte chunks of token u8 lie in an operand: groups 0, 1 (and 2, 3 in the next half)
+  const uint32_t at0 = w * 16 * 128 + u8 * 128 + ((c ^ u8) << 4), at1 = at0 ^ 64;
+
+  // the run's tiles in order, one ahead of the copies
+  int e = 0, n = 0;                 // tile of the unit, and the unit's tiles
+  int pages = 0, pages_next = 0;    // this warp's page numbers of 32 tiles, a lane each, and of the next 32
+  auto page_of = [&](int tile) {
+    const unsigned k0 = (unsigned)(place.s_begin + tile) * kKeys + w * 16;
+    return k0 < (unsigned)place.wk.held ? a.table[place.wk.r * a.table_stride + (k0 >> a.page_shift)] : -1;
+  };
+  auto next_tile = [&](Tile& x) {
+    if (e == n) {
+      if (n > 0) place.next(a, lane);
+      e = n = 0;
+      if (place.left <= 0) return false;
+      n = place.steps();
+      pages_next = page_of(lane);
+    }
+    if ((e & 31) == 0) {
+      pages = pages_next;
+      pages_next = page_of(e + 32 + lane);
+    }
+    const int page = __shfl_sync(0xffffffffu, pages, e & 31);
+    const unsigned k0 = (unsigned)(place.s_begin + e) * kKeys + w * 16;
+    x.keys = k0 < (unsigned)place.wk.held ? (int)min((unsigned)place.wk.held - k0, 16u) : 0;
+    x.src = x.keys > 0 && (unsigned)page < (unsigned)a.n_pages
+                ? a.cache + ((((size_t)page * a.Hkv + place.wk.h) << (a.page_shift - 4)) +
+                             ((k0 & ((1u << a.page_shift) - 1)) >> 4)) * c4::sub_bytes(D)
+                : nullptr;
+    x.first = e == 0;
+    if (e == 0) {
+      x.row0 = place.wk.row0;
+      x.h = place.wk.h;
+      x.t = place.wk.t;
+      x.rows = place.wk.rows();
+    }
+    e++;
+    return true;
+  };
+  auto copy = [&](const uint8_t* src, uint32_t dst) {
+    if (src)
+#pragma unroll
+      for (int at = 0; at < (int)L::piece; at += 512)
+        if (at + 512 <= (int)L::piece || at + lane * 16 < (int)L::piece)
+          cp_async16(dst + at + lane * 16, src + at + lane * 16);
+  };
+
+  Tile next, cur, prev;
+  bool has_next = next_tile(next), has_cur = false, has_prev = false, ok = true;
+  if (has_next) copy(next.src, raw_k);
+  cp_async_commit();
+  int units[2] = {0, 0};            // units so far that use rows of tile A, tile B
+  int g = 0;
+  for (;; g++) {
+    has_prev = has_cur;
+    has_cur = has_next;
+    if (!has_prev && !has_cur) break;
+    prev = cur;
+    cur = next;
+    ok = mbar_wait<2>(smem_addr(&sh.kv_empty[g & 1]), ((g >> 1) & 1) ^ 1, ab);
+    cp_async_wait_all();
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    uint32_t kx[2][NG], sc[2][NG / 2], lo[2][NG / 2], vx[2][NG], pair[2][NG];
+#pragma unroll
+    for (int it = 0; it < 2; it++) {
+      ld_shared(raw_v + (v8 + 8 * it) * 16 * NG + ((2 * c) ^ c4::v_turn(v8, NG)) * 2 * NG, vx[it]);
+      ld_shared(raw_v + (c4::vp_at(D) - c4::vc_at(D)) + (v8 + 8 * it) * 4 * NG, pair[it]);
+      ld_shared(raw_k + (u8 + 8 * it) * 16 * NG + c * 4 * NG, kx[it]);
+      ld_shared(raw_k + c4::ks_at(D) + (u8 + 8 * it) * 2 * NG, sc[it]);
+      ld_shared(raw_k + c4::km_at(D) + (u8 + 8 * it) * 2 * NG, lo[it]);
+    }
     __syncwarp();
-    sh.pages[w][lane] = ahead;
-    ahead = page_of(32 + lane);
-    __syncwarp();
-    int ip = 0, is = w;            // phase and piece that is copied next
-    auto issue = [&]() {
-      if (ip >= 2 * n) return;
-      const int tile = phase_tile(ip, n);
-      if (tile >= 4 * (batch + 1)) {
-        batch++;
-        sh.pages[w][32 * (batch & 1) + lane] = ahead;
-        ahead = page_of(32 * (batch + 1) + lane);
-        __syncwarp();
-      }
-      const int sub = tile * 8 + is;
-      const int k0 = s_begin * kKeys + sub * 16;
-      const int page = sh.pages[w][sub & 63];
-      const int slot = loads % kRing;
-      const bool there = (unsigned)k0 < (unsigned)held && (unsigned)page < (unsigned)a.n_pages;
-      bad = there ? bad & ~(1u << slot) : bad | (1u << slot);
-      if (lane == 0) {
-        const uint32_t bar = smem_addr(&sh.ring_full[w][slot]);
-        if (there) {
-          const uint8_t* src =
-              a.cache +
-              ((((size_t)page * a.Hkv + head) << (a.page_shift - 4)) + ((k0 & ((1 << a.page_shift) - 1)) >> 4)) *
-                  c4::sub_bytes(D) + (phase_is_k(ip, n) ? 0 : c4::vc_at(D));
-          mbar_arrive_expect_tx(bar, L::piece);
-          bulk_load(ring + slot * L::piece, src, L::piece, bar);
-        } else {
-          mbar_arrive(bar);
+    has_next = has_cur && next_tile(next);
+    if (has_next) copy(next.src, raw_k);
+    if (has_cur && cur.src) copy(cur.src + c4::vc_at(D), raw_v);
+    cp_async_commit();
+    if (has_prev) {
+      const uint32_t dst = smem + L::v + ((g - 1) & 1) * L::tile;
+#pragma unroll
+      for (int it = 0; it < 2; it++) {
+        // what lies behind the last key, or was never copied, must not reach the sums: 0 * NaN
+        const bool hide = !prev.src || u8 + 8 * it >= prev.keys;
+#pragma unroll
+        for (int j = 0; j < NG; j++) {
+          const uint32_t word = __byte_perm(vx[it][j / 2], vx[it][NG / 2 + j / 2], (j & 1) ? 0x7632u : 0x5410u);
+          const uint32_t pr = hide ? 0u : pair[it][j];
+          st_shared16(dst + (j >> 1) * L::half + ((j & 1) ? at1 : at0) + it * 8 * 128,
+                      values8(word, twice_lo(pr), twice_hi(pr)));
         }
-      }
-      loads++;
-      is += kFillWarps;
-      if (is >= 8) {
-        is -= 8;
-        ip++;
-      }
-    };
-    for (int k = 0; k < kRing; k++) issue();
-    bool queries = true;           // still to be brought in: after the first keys
-    for (int p = 0, s = w; p < 2 * n;) {
-      if (p > 0 && queries) {
-        queries = false;
-        const Walk wk = place.wk;
-        for (int t = 0; t < 2 && ok; t++) {
-          if (t == 1 && wk.rows() <= kRows) break;
-          QueryRows<D> qr;
-          qr.load(a, wk, t);
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.q_empty[t]), (units[t] & 1) ^ 1, ab));
-          if (!ok) break;
-          qr.store(a, smem + L::q + t * L::tile, sh.factor[units[t] & 1][t]);
-          fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&sh.q_full[t]));
-          units[t]++;
-        }
-        if (!ok) break;
-      }
-      const int tile = phase_tile(p, n);
-      const bool is_k = phase_is_k(p, n);
-      const int g = tiles_done + tile;               // operand buffer: g & 1, its use g / 2
-      const uint32_t empty = smem_addr(is_k ? &sh.k_empty[g & 1] : &sh.v_empty[g & 1]);
-      const int slot = used % kRing;
-      ok = mbar_wait(empty, ((g >> 1) & 1) ^ 1, ab) &&
-           mbar_wait(smem_addr(&sh.ring_full[w][slot]), (used / kRing) & 1, ab);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint32_t src = ring + slot * L::piece;
-      const bool none = (bad >> slot) & 1u;
-      const int k0 = (s_begin + tile) * kKeys + s * 16;
-      const uint32_t dst = smem + (is_k ? L::k : L::v) + (g & 1) * L::tile + s * 16 * 128;
-      if (is_k) {
-        uint32_t x[2][NG], sc[2][NG / 2], lo[2][NG / 2];
-#pragma unroll
-        for (int it = 0; it < 2; it++) {
-          const int u = u8 + 8 * it;
-          ld_shared(src + u * 16 * NG + c * 4 * NG, x[it]);
-          ld_shared(src + c4::ks_at(D) + u * 2 * NG, sc[it]);
-          ld_shared(src + c4::km_at(D) + u * 2 * NG, lo[it]);
-          // a page outside the cache: NaN, for every row that sees it
-          if (none)
-#pragma unroll
-            for (int j = 0; j < NG / 2; j++) sc[it][j] = 0x7e007e00u;
-        }
-#pragma unroll
-        for (int j = 0; j < NG; j++)
-#pragma unroll
-          for (int it = 0; it < 2; it++) {
-            const uint32_t s2 = sc[it][j / 2], l2 = lo[it][j / 2];
-            st_shared16(dst + (u8 + 8 * it) * 128 + (j >> 1) * L::half + (((4 * (j & 1) + c) ^ u8) << 4),
-                        (j & 1) ? values8(x[it][j], twice_hi(s2), twice_hi(l2))
-                                : values8(x[it][j], twice_lo(s2), twice_lo(l2)));
-          }
-      } else {
-        uint32_t x[2][NG], pair[2][NG];
-        bool hide[2];
-#pragma unroll
-        for (int it = 0; it < 2; it++) {
-          const int u = u8 + 8 * it, row = c4::v_row(u);
-          ld_shared(src + row * 16 * NG + ((2 * c) ^ c4::v_turn(row, NG)) * 2 * NG, x[it]);
-          ld_shared(src + (c4::vp_at(D) - c4::vc_at(D)) + row * 4 * NG, pair[it]);
-          // what lies behind the last key, or was never copied, must not reach the sums: 0 * NaN
-          hide[it] = none || (unsigned)(k0 + u) >= (unsigned)held;
-        }
-#pragma unroll
-        for (int j = 0; j < NG; j++)
-#pragma unroll
-          for (int it = 0; it < 2; it++) {
-            const uint32_t word = __byte_perm(x[it][j / 2], x[it][NG / 2 + j / 2], (j & 1) ? 0x7632u : 0x5410u);
-            const uint32_t pr = hide[it] ? 0u : pair[it][j];
-            st_shared16(dst + (u8 + 8 * it) * 128 + (j >> 1) * L::half + (((4 * (j & 1) + c) ^ u8) << 4),
-                        values8(word, twice_lo(pr), twice_hi(pr)));
-          }
-      }
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(is_k ? &sh.k_full[g & 1] : &sh.v_full[g & 1]));
-      used++;
-      issue();
-      s += kFillWarps;
-      if (s >= 8) {
-        s -= 8;
-        p++;
       }
     }
-    tiles_done += n;
-    place.next(a, lane);
+    if (has_cur) {
+      const uint32_t dst = smem + L::k + (g & 1) * L::tile;
+#pragma unroll
+      for (int it = 0; it < 2; it++)
+#pragma unroll
+        for (int j = 0; j < NG; j++) {
+          // a page outside the cache: NaN, for every row that sees it
+          const uint32_t s2 = cur.src ? sc[it][j / 2] : 0x7e007e00u, l2 = lo[it][j / 2];
+          st_shared16(dst + (j >> 1) * L::half + ((j & 1) ? at1 : at0) + it * 8 * 128,
+                      (j & 1) ? values8(kx[it][j], twice_hi(s2), twice_hi(l2))
+                              : values8(kx[it][j], twice_lo(s2), twice_lo(l2)));
+        }
+    }
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&sh.kv_full[g & 1]));
+    if (has_cur && cur.first) {     // the unit's queries, after its first keys
+#pragma unroll 1
+      for (int t = 0; t < (cur.rows > kRows ? 2 : 1); t++) {
+        const int k = t ? units[1] : units[0];
+        QueryRows<D> qr;
+        qr.load(a, cur, t);
+        ok = __all_sync(0xffffffffu, mbar_wait<2>(smem_addr(&sh.q_empty[t]), (k & 1) ^ 1, ab));
+        if (!ok) break;
+        qr.store(a, smem + L::q + t * L::tile, sh.factor[k & 1][t]);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.q_full[t]));
+        t ? units[1]++ : units[0]++;
+      }
+      if (!ok) break;
+    }
   }
-  // copies in flight land before the CTA exits
-  for (int i = used; i < loads; i++)
-    mbar_wait_drain(smem_addr(&sh.ring_full[w][i % kRing]), (i / kRing) & 1, a.status, kWaitLimitNs);
+  cp_async_wait_all();
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -555,16 +536,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
       mbar_init(smem_addr(&sh.q_full[s]), kFillWarps);
       // the last QK^T has read Q, and each softmax warp its factors
       mbar_init(smem_addr(&sh.q_empty[s]), 1 + 4);
-      mbar_init(smem_addr(&sh.k_full[s]), 8);
-      mbar_init(smem_addr(&sh.v_full[s]), 8);
-      mbar_init(smem_addr(&sh.k_empty[s]), 1);
-      mbar_init(smem_addr(&sh.v_empty[s]), 1);
+      mbar_init(smem_addr(&sh.kv_full[s]), kFillWarps);
+      mbar_init(smem_addr(&sh.kv_empty[s]), 1);
       mbar_init(smem_addr(&sh.s_full[s]), 1);
       mbar_init(smem_addr(&sh.p_full[s]), kRows);
       mbar_init(smem_addr(&sh.o_final[s]), 1);
     }
-    for (int w = 0; w < kFillWarps; w++)
-      for (int s = 0; s < kRing; s++) mbar_init(smem_addr(&sh.ring_full[w][s]), 1);
     mbar_init(smem_addr(&sh.drain), 1);
     fence_barrier_init();
   }
@@ -613,7 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
   if (lane == 0) place = Place{wk, s_begin, left, sh.line0, chunk};
   __syncwarp();
 
-  if (warp <= kFillWarps) {
+  if (warp < kFill0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == 0) {
       // ---------------------------------------------------------------- MMA issuer
       const uint32_t idesc_qk = idesc_f16_f32(kRows, kKeys, false);
@@ -637,13 +615,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
           two = place.wk.rows() > kRows;
         }
         const int gp = g - 1;
-        if (pv) ok = mbar_wait(smem_addr(&sh.v_full[gp & 1]), (gp >> 1) & 1, ab);
+        ok = mbar_wait(smem_addr(&sh.kv_full[g & 1]), (g >> 1) & 1, ab);
         const uint64_t dKj = dK + (uint64_t)((g & 1) * kTileDesc), dVj = dV + (uint64_t)((gp & 1) * kTileDesc);
 #pragma unroll
         for (int t = 0; t < 2; t++) {
           const uint32_t tS = tmem + t * 128, tO = tmem + 256 + t * D;
           if (pv && (t == 0 || pv_two)) {
-            ok = ok && mbar_wait(smem_addr(&sh.p_full[t]), (t ? p1++ : p0++) & 1, ab);
+            ok = ok && mbar_wait(smem_addr(&sh.p_full[t]), (t ? p1 : p0) & 1, ab);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -651,12 +629,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
             for (int kk = 0; kk < kKeys / 16; kk++)
               mma_ts_elect(tO, tS + (kk >> 2) * 64 + (kk & 3) * 8, dVj + (uint64_t)(kk * (2048 >> 4)), idesc_pv,
                            kk ? 1u : (uint32_t)pv_on);
+            t ? p1++ : p0++;
             if (pv_last) mma_commit_elect(smem_addr(&sh.o_final[t]));
           }
-          if (t == 1 && pv) mma_commit_elect(smem_addr(&sh.v_empty[gp & 1]));
           if (!flush && (t == 0 || two)) {
             if (j == 0) ok = ok && mbar_wait(smem_addr(&sh.q_full[t]), (t ? units1 : units0) & 1, ab);
-            if (t == 0) ok = ok && mbar_wait(smem_addr(&sh.k_full[g & 1]), (g >> 1) & 1, ab);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -674,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
           }
         }
         if (!ok || flush) break;
-        mma_commit_elect(smem_addr(&sh.k_empty[g & 1]));
+        mma_commit_elect(smem_addr(&sh.kv_empty[g & 1]));
         pv = true;
         pv_two = two;
         pv_on = j > 0;
@@ -688,16 +665,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
       mma_commit_elect(smem_addr(&sh.drain));
       mbar_wait_drain(smem_addr(&sh.drain), 0, a.status, kWaitLimitNs);
       __syncwarp();
-    } else {
-      fill<D>(a, sh, smem, place, ab);
     }
+  } else if (warp < kSoft0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFill));
+    fill<D>(a, sh, smem, place, ab);
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ------------------------------------------------------------------ softmax and O
-    const int t = (warp - kFillWarps - 1) >> 2, quarter = warp & 3;
+    const int t = (warp - kSoft0) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + lanes + t * 128, tO = tmem + lanes + 256 + t * D;
-    const bool scribe = threadIdx.x == 32 * (1 + kFillWarps);   // writes the CTA's entry of the join list
+    const bool scribe = threadIdx.x == 32 * kSoft0;   // writes the CTA's entry of the join list
     if (scribe) a.joins[2 * cta] = make_int4(0, 0, 0, 0);   // none, so far
     uint32_t scnt = 0;
     int unit = 0;
@@ -719,13 +698,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
       }
       if (used) {
         float m = -INFINITY, l = 0.f;
-        bool ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.q_full[t]), unit & 1, ab));
+        bool ok = __all_sync(0xffffffffu, mbar_wait<1>(smem_addr(&sh.q_full[t]), unit & 1, ab));
         if (!ok) break;
         const float factor = sh.factor[unit & 1][t][row];
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.q_empty[t]));
         for (int j = 0; j < n; j++, scnt++, seen -= kKeys) {
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.s_full[t]), scnt & 1, ab));
+          ok = __all_sync(0xffffffffu, mbar_wait<1>(smem_addr(&sh.s_full[t]), scnt & 1, ab));
           if (!ok) break;
           tc_fence_after();
           const bool cut = __any_sync(0xffffffffu, seen < kKeys);
@@ -775,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
           tc_fence_before();
           mbar_arrive(smem_addr(&sh.p_full[t]));
         }
-        ok = ok && mbar_wait(smem_addr(&sh.o_final[t]), unit & 1, ab);
+        ok = ok && mbar_wait<1>(smem_addr(&sh.o_final[t]), unit & 1, ab);
         unit++;
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
@@ -885,6 +864,11 @@ cudaError_t go(Cache4AttnArgs a, cudaStream_t st) {
   auto kernel = cache4_tc_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::bytes);
   if (e != cudaSuccess) return e;
+  // setmaxnreg.inc waits until the registers it asks for are free: refuse to launch unless the split
+  // fits what the launch hands out
+  cudaFuncAttributes fa;
+  if ((e = cudaFuncGetAttributes(&fa, kernel))) return e;
+  if (kRegsIssue + 2 * kRegsFill + 2 * kRegsSoftmax > 5 * fa.numRegs) return cudaErrorInvalidConfiguration;
   kernel<<<kCache4TcCtas, kThreads, Layout<D>::bytes, st>>>(a);
   if ((e = cudaGetLastError())) return e;
   cache4_tc_join_kernel<D><<<dim3(kCache4TcCtas, 2 * kRows / 32), 256, 0, st>>>(a);
