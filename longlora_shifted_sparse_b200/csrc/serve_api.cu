@@ -150,7 +150,7 @@ s2_status s2attn_page_plan(const int* cached_lens, const int* new_lens, const in
 
 size_t s2attn_cache4_bytes(int n_pages, int page_size, int H_kv, int d) {
   const int shift = page_shift(page_size);
-  if (shift < 0 || H_kv <= 0 || !headdim32_ok(d) || !cache_ok(n_pages, page_size)) return 0;
+  if (shift < 0 || H_kv <= 0 || H_kv > 65535 || !headdim32_ok(d) || !cache_ok(n_pages, page_size)) return 0;
   return ((size_t)n_pages * H_kv << (shift - 4)) * c4::sub_bytes(d);
 }
 
@@ -160,7 +160,7 @@ s2_status s2attn_cache4_append(const void* k, const void* v, void* cache, const 
                                void* cuda_stream) {
   if (!k || !v || !cache || !slots || !k_strides || !v_strides) return S2_ERR_NULL;
   if (!dtype_ok(dtype)) return S2_ERR_DTYPE;
-  if (T <= 0 || H_kv <= 0 || !cache_ok(n_pages, page_size)) return S2_ERR_SHAPE;
+  if (T <= 0 || H_kv <= 0 || H_kv > 65535 || !cache_ok(n_pages, page_size)) return S2_ERR_SHAPE;
   if (!headdim32_ok(d)) return S2_ERR_HEADDIM;
   const int shift = page_shift(page_size);
   if (shift < 0) return S2_ERR_ARG;
@@ -185,7 +185,7 @@ s2_status s2attn_cache4_read(const void* cache, const int* slots, void* k, void*
                              void* cuda_stream) {
   if (!k || !v || !cache || !slots) return S2_ERR_NULL;
   if (!dtype_ok(dtype)) return S2_ERR_DTYPE;
-  if (T <= 0 || H_kv <= 0 || !cache_ok(n_pages, page_size)) return S2_ERR_SHAPE;
+  if (T <= 0 || H_kv <= 0 || H_kv > 65535 || !cache_ok(n_pages, page_size)) return S2_ERR_SHAPE;
   if (!headdim32_ok(d)) return S2_ERR_HEADDIM;
   const int shift = page_shift(page_size);
   if (shift < 0) return S2_ERR_ARG;
