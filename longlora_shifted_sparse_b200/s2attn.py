@@ -14,6 +14,7 @@ fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -156,12 +157,11 @@ def check(status: int) -> None:
 # ----------------------------------------------------------------------------- torch layer
 
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return S2_BF16
-    if t.dtype == torch.float32:
-        return S2_FP32
-    raise TypeError("s2attn supports bfloat16 and float32 tensors, got %s" % t.dtype)
+    _torch or _lazy()
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError("s2attn supports bfloat16 and float32 tensors, got %s" % t.dtype)
+    return code
 
 
 def _stream_ptr(device) -> int:
@@ -299,15 +299,32 @@ def s2_attention(q, k, v, G: int, pi_scale: float, rope_base: float = 10000.0,
 # ----------------------------------------------------------------------------- serving
 #
 # Calls on tensors of another device than the current one make that device current for the
-# launch; work goes to that device's current stream.
+# launch; work goes to that device's current stream. These calls run once per layer and token, so
+# their host time counts: torch's names are looked up once, checks are one expression each on
+# the way that succeeds, and stride arrays are kept by value.
+
+_torch = None
+
+
+def _lazy():
+    """torch, imported on the first call, with the names that every call needs."""
+    global _torch, _device_now, _raw_stream, _i32, _DTYPES
+    import torch
+    _device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _i32, _DTYPES = torch.int32, {torch.bfloat16: S2_BF16, torch.float32: S2_FP32}
+    _torch = torch
+    return torch
+
 
 def _call(device, fn, *args) -> None:
-    import torch
-    if device.index == torch.cuda.current_device():
-        check(fn(*args, _stream_ptr(device)))
+    index = device.index
+    if index is not None and index == _device_now():
+        status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            check(fn(*args, _stream_ptr(device)))
+        with _torch.cuda.device(device):
+            status = fn(*args, _stream_ptr(device))
+    if status:
+        raise S2Error(status)
 
 
 def _need(ok: bool, what: str) -> None:
@@ -316,17 +333,28 @@ def _need(ok: bool, what: str) -> None:
 
 
 def _ints(t, name, device, shape=None):
-    """A dense int32 CUDA tensor of this device (and shape)."""
-    import torch
-    if t.dtype is not torch.int32:
+    """Address of a dense int32 CUDA tensor of this device (and shape)."""
+    if t.dtype is _i32 and t.device == device and t.is_contiguous() and (shape is None or t.shape == shape):
+        return t.data_ptr()
+    if t.dtype is not _i32:
         raise TypeError("%s must be int32, got %s" % (name, t.dtype))
     _need(t.device == device, "%s is on %s, not on %s" % (name, t.device, device))
-    _need(t.is_contiguous() and (shape is None or tuple(t.shape) == shape),
-          "%s must be dense%s" % (name, "" if shape is None else " with shape %s" % (shape,)))
-    return t.data_ptr()
+    raise ValueError("%s must be dense%s" % (name, "" if shape is None else " with shape %s" % (shape,)))
 
 
-_ll2, _ll3 = _ll * 2, _ll * 3
+def _table(t, device, R):
+    """Columns and row stride of a block table of R requests."""
+    if t.dtype is not _i32:
+        raise TypeError("block_table must be int32, got %s" % t.dtype)
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != R or t.device != device or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("block_table must be [R, max_pages] on %s with dense rows" % device)
+    return shape[1], max(t.stride(0), shape[1])
+
+
+@functools.lru_cache(maxsize=512)
+def _strides(*s):
+    return (_ll * len(s))(*s)
 
 
 def rope_freqs(rotary_dim: int, rope_base: float = 10000.0, pi_scale: float = 1.0,
@@ -344,47 +372,73 @@ def rope_freqs(rotary_dim: int, rope_base: float = 10000.0, pi_scale: float = 1.
 
 
 def _rope_rows(x, name):
-    """x as [B, N, H, d] (a [T, H, d] tensor is one batch entry) with dense channels."""
-    _need(x.dim() in (3, 4), "%s must be [T, H, d] or [B, N, H, d], got %s" % (name, tuple(x.shape)))
-    x = x if x.dim() == 4 else x.unsqueeze(0)
-    return x if x.stride(-1) == 1 and x.data_ptr() % 16 == 0 else x.contiguous()
+    """x with dense, 16-byte aligned channels, and its strides of batch, token and head (a [T, H, d]
+    tensor is one batch entry)."""
+    st = x.stride()
+    if st[-1] != 1 or x.data_ptr() % 16:
+        x = x.contiguous()
+        st = x.stride()
+    return x, _strides(st[0], st[1], st[2]) if len(st) == 4 else _strides(0, st[0], st[1])
 
 
 def _rope_launch(q, k, positions, freqs, layout, mscale, inverse, in_place):
-    import torch
-    dt = _dtype_code(q)
-    q4 = _rope_rows(q, "q")
-    B, N, Hq, d = q4.shape
-    pos = positions if positions.dim() == 2 else positions.unsqueeze(0)
-    if pos.dtype not in (torch.int32, torch.int64):
+    torch = _torch or _lazy()
+    dt, dev, shape = _DTYPES.get(q.dtype), q.device, q.shape
+    if dt is None:
+        _dtype_code(q)
+    nd = len(shape)
+    if nd == 4:
+        B, N, Hq, d = shape
+    else:
+        _need(nd == 3, "q must be [T, H, d] or [B, N, H, d], got %s" % (tuple(shape),))
+        (N, Hq, d), B = shape, 1
+    wide = positions.dtype is torch.int64
+    if not wide and positions.dtype is not _i32:
         raise TypeError("positions must be int32 or int64, got %s" % positions.dtype)
-    if freqs.dtype != torch.float64:
+    if freqs.dtype is not torch.float64:
         raise TypeError("freqs must be float64 (see rope_freqs), got %s" % freqs.dtype)
-    _need(pos.dim() == 2 and pos.shape[1] == N and pos.shape[0] in (1, B),
-          "positions must be [N] or [B, N], got %s" % (tuple(positions.shape),))
+    pshape, pst = positions.shape, positions.stride()
+    if len(pshape) == 1 and pshape[0] == N:
+        pst = _strides(0, pst[0])
+    else:
+        _need(len(pshape) == 2 and pshape[1] == N and pshape[0] in (1, B),
+              "positions must be [N] or [B, N], got %s" % (tuple(pshape),))
+        pst = _strides(0 if pshape[0] == 1 else pst[0], pst[1])
     _need(freqs.dim() == 1 and freqs.is_contiguous(), "freqs must be one dense row")
-    _need(q.device == pos.device == freqs.device, "q, positions and freqs must share a device")
-    out = q if in_place else torch.empty_like(q4, memory_format=torch.contiguous_format)
-    _need(not in_place or q4.data_ptr() == q.data_ptr(),
-          "in place needs dense, 16-byte aligned channels")
-    k4 = kout = None
+    _need(dev == positions.device == freqs.device, "q, positions and freqs must share a device")
+    q4, qst = _rope_rows(q, "q")
+    out = q if in_place else torch.empty(shape, dtype=q.dtype, device=dev)
+    kp = kop = kst = kout = None
+    Hkv = 0
+    same = q4 is q
     if k is not None:
-        _need(k.dtype == q.dtype and k.device == q.device, "q and k must share dtype and device")
-        k4 = _rope_rows(k, "k")
-        _need(k4.shape[:2] == q4.shape[:2] and k4.shape[3] == d and k.dim() == q.dim(),
-              "q %s and k %s must share all but heads" % (tuple(q.shape), tuple(k.shape)))
-        kout = k if in_place else torch.empty_like(k4, memory_format=torch.contiguous_format)
-        _need(not in_place or k4.data_ptr() == k.data_ptr(),
-              "in place needs dense, 16-byte aligned channels")
-    if q4.numel() or (k4 is not None and k4.numel()):
-        _call(q.device, s2attn_rope, q4.data_ptr(), out.data_ptr(),
-              None if k is None else k4.data_ptr(), None if k is None else kout.data_ptr(),
-              pos.data_ptr(), pos.dtype == torch.int64, freqs.data_ptr(), B, N, Hq,
-              0 if k is None else k4.shape[2], d, 2 * freqs.numel(), _ll3(*q4.stride()[:3]),
-              None if k is None else _ll3(*k4.stride()[:3]),
-              _ll2(0 if pos.shape[0] == 1 else pos.stride(0), pos.stride(1)),
+        kshape = k.shape
+        _need(k.dtype is q.dtype and k.device == dev, "q and k must share dtype and device")
+        _need(len(kshape) == nd and kshape[-1] == d and kshape[:-2] == shape[:-2],
+              "q %s and k %s must share all but heads" % (tuple(shape), tuple(kshape)))
+        k4, kst = _rope_rows(k, "k")
+        same = same and k4 is k
+        kout = k if in_place else torch.empty(kshape, dtype=k.dtype, device=dev)
+        Hkv, kp, kop = kshape[-2], k4.data_ptr(), kout.data_ptr()
+    if in_place:
+        _need(same, "in place needs dense, 16-byte aligned channels")
+        _need(all(not _overlaps(x) for x in (q, k) if x is not None), "in place needs rows that do not overlap")
+    if B * N * (Hq + Hkv):
+        _call(dev, s2attn_rope, q4.data_ptr(), out.data_ptr(), kp, kop, positions.data_ptr(), wide,
+              freqs.data_ptr(), B, N, Hq, Hkv, d, 2 * freqs.shape[0], qst, kst, pst,
               ROPE_LAYOUTS[layout], inverse, mscale, dt)
-    return out.view(q.shape), None if k is None else kout.view(k.shape)
+    return out, kout
+
+
+def _overlaps(x) -> bool:
+    """True where two elements of x may share an address."""
+    reach = 0
+    for stride, size in sorted(zip(x.stride(), x.shape)):
+        if size > 1:
+            if stride <= reach:
+                return True
+            reach += (size - 1) * stride
+    return False
 
 
 _rope_fn = None
@@ -420,10 +474,9 @@ def rope(q, k, positions, freqs, layout: str = "interleaved", mscale: float = 1.
     channels (2i, 2i+1) ("interleaved", as in the attention calls) or (i, i + half)
     ("half"). mscale multiplies the rotated channels. Differentiable in q and k;
     in_place=True overwrites them instead and has no gradient."""
-    import torch
     if layout not in ROPE_LAYOUTS:
         raise ValueError("layout must be one of %s, got %r" % (sorted(ROPE_LAYOUTS), layout))
-    grad = torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad))
+    grad = (q.requires_grad or (k is not None and k.requires_grad)) and (_torch or _lazy()).is_grad_enabled()
     if not grad:
         return _rope_launch(q, k, positions, freqs, layout, mscale, False, in_place)
     _need(not in_place, "in_place=True has no gradient")
@@ -454,23 +507,17 @@ def page_plan(cached_lens, new_lens, free_pages, free_count, block_table, page_s
     in rows that no request owns), free_count [1] (what is left) and left_out [1]: the number
     of requests that did not fit (too long for the table or for max_tokens, or no pages left),
     whose slots are -1 and whose lengths stay."""
-    import torch
-    dev = cached_lens.device
-    R = cached_lens.numel()
+    torch = _torch or _lazy()
+    dev, R = cached_lens.device, cached_lens.numel()
     c, n = _ints(cached_lens, "cached_lens", dev, (R,)), _ints(new_lens, "new_lens", dev, (R,))
     f, fc = _ints(free_pages, "free_pages", dev), _ints(free_count, "free_count", dev, (1,))
-    if block_table.dtype is not torch.int32:
-        raise TypeError("block_table must be int32, got %s" % block_table.dtype)
-    _need(block_table.device == dev and block_table.dim() == 2 and block_table.shape[0] == R and
-          (block_table.stride(1) == 1 or block_table.shape[1] <= 1),
-          "block_table must be [R, max_pages] on %s with dense rows" % dev)
-    out = torch.empty(2 * R + 1 + 2 * max_tokens + 2, dtype=torch.int32, device=dev)
-    cu, lens, pos, slots, free_left, left_out = out.split((R + 1, R, max_tokens, max_tokens, 1, 1))
+    cols, stride = _table(block_table, dev, R)
+    out = torch.empty(2 * R + 3 + 2 * max_tokens, dtype=_i32, device=dev)
     p, b = out.data_ptr(), 4 * (2 * R + 1)
     _call(dev, s2attn_page_plan, c, n, f, fc, block_table.data_ptr(), p, p + 4 * (R + 1), p + b,
-          p + b + 4 * max_tokens, p + b + 8 * max_tokens, R, max_tokens, free_pages.numel(),
-          block_table.shape[1], max(block_table.stride(0), block_table.shape[1]), page_size)
-    return PagePlan(cu, lens, pos, slots, free_left, left_out)
+          p + b + 4 * max_tokens, p + b + 8 * max_tokens, R, max_tokens, free_pages.numel(), cols,
+          stride, page_size)
+    return PagePlan(*out.split_with_sizes((R + 1, R, max_tokens, max_tokens, 1, 1)))
 
 
 def cache4(n_pages: int, page_size: int, Hkv: int, d: int, device="cuda"):
@@ -483,43 +530,52 @@ def cache4(n_pages: int, page_size: int, Hkv: int, d: int, device="cuda"):
 
 def _cache4_shape(cache):
     """(n_pages, page_size, Hkv, d) of a cache tensor."""
-    import torch
-    _need(cache.dtype is torch.uint8 and cache.dim() == 4 and cache.is_contiguous() and
-          cache.shape[3] % 20 == 0, "cache must be a tensor that cache4() made")
-    n_pages, Hkv, subs, width = cache.shape
-    return n_pages, 16 * subs, Hkv, width // 20
+    torch = _torch or _lazy()
+    shape = cache.shape
+    if cache.dtype is not torch.uint8 or len(shape) != 4 or shape[3] % 20 or not cache.is_contiguous():
+        raise ValueError("cache must be a tensor that cache4() made")
+    return shape[0], 16 * shape[2], shape[1], shape[3] // 20
+
+
+def _cache4_rows(x):
+    """x [T, H, d] with rows of 16-byte pieces, and its strides of token and head."""
+    s0, s1, s2 = x.stride()
+    if s2 != 1 or (x.data_ptr() | (s0 | s1) * x.element_size()) % 16:
+        x = x.contiguous()
+        s0, s1, s2 = x.stride()
+    return x, _strides(s0, s1)
 
 
 def cache4_append(k, v, cache, slots) -> None:
     """Stores k, v [T, Hkv, d] in the cache's slots (int32 [T]; rows with a negative slot, or one
     beyond the cache, are skipped; the others must differ)."""
     n_pages, P, Hkv, d = _cache4_shape(cache)
-    _need(k.dim() == 3 and k.shape == v.shape and tuple(k.shape[1:]) == (Hkv, d),
-          "k %s and v %s must be [T, %d, %d]" % (tuple(k.shape), tuple(v.shape), Hkv, d))
-    _need(k.dtype == v.dtype and k.device == v.device == cache.device,
+    dev, shape = cache.device, k.shape
+    _need(len(shape) == 3 and shape == v.shape and shape[1] == Hkv and shape[2] == d,
+          "k %s and v %s must be [T, %d, %d]" % (tuple(shape), tuple(v.shape), Hkv, d))
+    _need(k.dtype is v.dtype and k.device == dev and v.device == dev,
           "k, v must share a dtype, and their device with the cache")
-    T, dt = k.shape[0], _dtype_code(k)
-    at = _ints(slots, "slots", cache.device, (T,))
-    if T == 0:
-        return
-    k, v = (x if x.stride(2) == 1 and (x.data_ptr() | (x.stride(0) | x.stride(1)) * x.element_size())
-            % 16 == 0 else x.contiguous() for x in (k, v))
-    _call(cache.device, s2attn_cache4_append, k.data_ptr(), v.data_ptr(), cache.data_ptr(), at, T,
-          Hkv, d, n_pages, P, _ll2(*k.stride()[:2]), _ll2(*v.stride()[:2]), dt)
+    T, dt = shape[0], _dtype_code(k)
+    at = _ints(slots, "slots", dev, (T,))
+    if T:
+        k, ks = _cache4_rows(k)
+        v, vs = _cache4_rows(v)
+        _call(dev, s2attn_cache4_append, k.data_ptr(), v.data_ptr(), cache.data_ptr(), at, T, Hkv, d,
+              n_pages, P, ks, vs, dt)
 
 
 def cache4_read(cache, slots, dtype=None):
     """(k, v) [T, Hkv, d] that the slots (int32 [T]) hold, in bfloat16 or float32; slots outside
     the cache give zeros."""
-    import torch
     n_pages, P, Hkv, d = _cache4_shape(cache)
-    T = slots.numel()
-    at = _ints(slots, "slots", cache.device, (T,))
-    k = torch.empty(T, Hkv, d, dtype=dtype or torch.bfloat16, device=cache.device)
-    v = torch.empty_like(k)
+    dev, T = cache.device, slots.numel()
+    at = _ints(slots, "slots", dev, (T,))
+    k = _torch.empty((T, Hkv, d), dtype=dtype or _torch.bfloat16, device=dev)
+    v = _torch.empty_like(k)
+    dt = _dtype_code(k)
     if T:
-        _call(cache.device, s2attn_cache4_read, cache.data_ptr(), at, k.data_ptr(), v.data_ptr(), T,
-              Hkv, d, n_pages, P, _dtype_code(k))
+        _call(dev, s2attn_cache4_read, cache.data_ptr(), at, k.data_ptr(), v.data_ptr(), T, Hkv, d,
+              n_pages, P, dt)
     return k, v
 
 
@@ -540,34 +596,27 @@ def cache4_attention(q, cache, block_table, lens, cu_new, max_new: int, scale=No
     by default. ws: ``cache4_workspace``, made anew where it is None. Returns o [T, Hq, d]
     (out, if given, whose rows that no request owns stay as they were), or (o, lse) with lse
     [Hq, T]. A row that sees no key gets 0 and -inf."""
-    import torch
     n_pages, P, Hkv, d = _cache4_shape(cache)
-    dev = cache.device
-    _need(q.dim() == 3 and q.shape[2] == d and q.device == dev,
-          "q must be [T, Hq, %d] on %s, got %s on %s" % (d, dev, tuple(q.shape), q.device))
-    T, Hq, _ = q.shape
+    dev, shape = cache.device, q.shape
+    _need(len(shape) == 3 and shape[2] == d and q.device == dev,
+          "q must be [T, Hq, %d] on %s, got %s on %s" % (d, dev, tuple(shape), q.device))
+    T, Hq, _ = shape
     dt, R = _dtype_code(q), lens.numel()
     ln, cu = _ints(lens, "lens", dev, (R,)), _ints(cu_new, "cu_new", dev, (R + 1,))
-    if block_table.dtype is not torch.int32:
-        raise TypeError("block_table must be int32, got %s" % block_table.dtype)
-    _need(block_table.device == dev and block_table.dim() == 2 and block_table.shape[0] == R and
-          (block_table.stride(1) == 1 or block_table.shape[1] <= 1),
-          "block_table must be [R, max_pages] on %s with dense rows" % dev)
-    if q.stride(2) != 1 or (q.data_ptr() | (q.stride(0) | q.stride(1)) * q.element_size()) % 16:
-        q = q.contiguous()
+    cols, stride = _table(block_table, dev, R)
+    q, qs = _cache4_rows(q)
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
+        out = _torch.empty(shape, dtype=q.dtype, device=dev)
     else:
-        _need(out.shape == q.shape and out.dtype == q.dtype and out.device == dev and
+        _need(out.shape == shape and out.dtype is q.dtype and out.device == dev and
               out.is_contiguous(), "out must be a dense tensor like q")
-    lse = torch.empty((Hq, T), dtype=torch.float32, device=dev) if return_lse else None
+    lse = _torch.empty((Hq, T), dtype=_torch.float32, device=dev) if return_lse else None
     if ws is None:
         ws = cache4_workspace(dev)
     _need(ws.device == dev, "ws is on %s, not on %s" % (ws.device, dev))
     if T:
         _call(dev, s2attn_cache4_attn, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), ln, cu,
               out.data_ptr(), None if lse is None else lse.data_ptr(), R, T, Hq, Hkv, d, n_pages, P,
-              block_table.shape[1], max(block_table.stride(0), block_table.shape[1]),
-              _ll2(q.stride(0), q.stride(1)), max_new, d ** -0.5 if scale is None else scale, dt,
-              ws.data_ptr(), ws.numel())
+              cols, stride, qs, max_new, d ** -0.5 if scale is None else scale, dt, ws.data_ptr(),
+              ws.numel())
     return (out, lse) if return_lse else out
