@@ -9,9 +9,9 @@
 // instructions want at least 64 rows and operands in shared memory, which a dozen query rows
 // cannot use and which would send each dequantised value through shared memory once more.
 //
-// k codes become fp16 operands by one logic operation for two (a code in the low bits of an
-// fp16 1024 is 1024 + code, in the next four bits 1024 + 16 code): the 16 is taken out of the
-// query's half of those channels, the 1024 by starting the sum at minus its part. A group's
+// k codes become fp16 operands by one logic operation for two: a code in the low bits of an fp16
+// is the subnormal code 2^-24, in the next four bits 16 times that, which is taken out of the
+// query's half of those channels; the 2^-24 goes into the scores' factor. A group's
 // products with the codes are exact, its sum is fp32; its scale is applied to the sum, the
 // minima go through one more MMA against the queries' sums over each group (split in two
 // fp16 parts, which carry 22 bits). A query row is first scaled by a power of two so that fp16
@@ -113,7 +113,6 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[NG]) 
 template <int NG, int NT>
 struct Queries {
   uint4 frag[NT][NG][32];   // B operands: of a group's two k-steps
-  float start[NT][NG][8];   // minus the offset's part of a group's sum
   uint2 sums[NT][32];       // B operand of the minima
   float factor[NT * 8];     // score factor, log2 domain
   int keys[NT * 8];         // keys that the row sees
@@ -245,28 +244,23 @@ __global__ void __launch_bounds__(kThreads, MINB) cache4_attn_kernel(const __gri
       // below 2^14), from its exponent
       const int ex = max((int)(__float_as_uint(big) >> 23), 9);
       const float down = __uint_as_float((uint32_t)(262 - ex) << 23), up = __uint_as_float((uint32_t)(ex - 8) << 23);
-      float part[NG], off[NG];
+      float part[NG];
 #pragma unroll
       for (int j = 0; j < NG; j++) {
-        part[j] = off[j] = 0.f;
+        part[j] = 0.f;
         __half y[8];
 #pragma unroll
         for (int e = 0; e < 8; e++) {
           const float xe = x[j][e] * down;
           y[e] = __float2half_rn((e & 1) ? xe * 0.0625f : xe);
           const float ye = __half2float(y[e]);
-          off[j] -= 1024.f * ye;
           part[j] += (e & 1) ? 16.f * ye : ye;
         }
         const __half2 f[4] = {__halves2half2(y[0], y[4]), __halves2half2(y[1], y[5]),
                               __halves2half2(y[2], y[6]), __halves2half2(y[3], y[7])};
         sm.q.frag[nt][j][lane] = *reinterpret_cast<const uint4*>(f);
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          part[j] += __shfl_xor_sync(0xffffffffu, part[j], o);
-          off[j] += __shfl_xor_sync(0xffffffffu, off[j], o);
-        }
-        if (c == 0) sm.q.start[nt][j][g] = off[j];
+        for (int o = 1; o < 4; o <<= 1) part[j] += __shfl_xor_sync(0xffffffffu, part[j], o);
       }
       // groups 2c, 2c + 1 of this row: high parts against the first eight k, low ones after
       float s0 = 0.f, s1 = 0.f;
@@ -278,20 +272,16 @@ __global__ void __launch_bounds__(kThreads, MINB) cache4_attn_kernel(const __gri
       const float h0 = __half2float(__float2half_rn(s0)), h1 = __half2float(__float2half_rn(s1));
       sm.q.sums[nt][lane] = make_uint2(pack_half2(h0, h1), pack_half2(s0 - h0, s1 - h1));
       if (c == 0) {
-        sm.q.factor[nt * 8 + g] = up * a.scale * 1.4426950408889634f;
+        sm.q.factor[nt * 8 + g] = up * a.scale * (1.4426950408889634f * 0x1p24f);
         sm.q.keys[nt * 8 + g] = live ? max(0, rq.held - (rq.n - 1 - i)) : see_max;
       }
     }
     __syncthreads();
 
     uint4 qreg[NT == 1 ? NG : 1];
-    float2 qstart[NT == 1 ? NG : 1];
     if constexpr (NT == 1) {
 #pragma unroll
-      for (int j = 0; j < NG; j++) {
-        qreg[j] = sm.q.frag[0][j][lane];
-        qstart[j] = *reinterpret_cast<const float2*>(&sm.q.start[0][j][2 * c]);
-      }
+      for (int j = 0; j < NG; j++) qreg[j] = sm.q.frag[0][j][lane];
     }
 
     float O[2 * NG][NT][4], m[NT][2], l[NT][2];
@@ -326,15 +316,21 @@ __global__ void __launch_bounds__(kThreads, MINB) cache4_attn_kernel(const __gri
         const bool ok0 = (unsigned)page0 < (unsigned)a.n_pages;
         const bool ok1 = (unsigned)page1 < (unsigned)a.n_pages;
         bad |= ((ok0 ? 0u : 1u) | (ok1 ? 0u : 2u)) << (2 * slot);
-        const uint8_t* src0 = a.cache + ((((size_t)page0 * a.Hkv + h) << (a.page_shift - 4)) + in_page) * SUB;
+        const uint8_t* src0 = a.cache + ((((size_t)page0 * a.Hkv + h) << (a.page_shift - 4)) + in_page) * SUB + lane * 16;
         const uint8_t* src1 = a.cache + ((((size_t)page1 * a.Hkv + h) << (a.page_shift - 4)) +
-                                         (a.page_shift == 4 ? 0 : in_page + 1)) * SUB;
-        const uint32_t dst = ring_at + slot * (2 * SUB);
+                                         (a.page_shift == 4 ? 0 : in_page + 1)) * SUB + lane * 16;
+        const uint32_t dst = ring_at + slot * (2 * SUB) + lane * 16;
+        // a sub-block is FULL copies of 512 bytes, and the rest by the first lanes
+        constexpr int FULL = SUB / 512, REST = SUB % 512 / 16;
+        if (ok0) {
 #pragma unroll
-        for (int i = 0; i < 2 * SUB / 512; i++) {
-          const int at = i * 512 + lane * 16;
-          const bool second = at >= SUB;
-          if (second ? ok1 : ok0) cp_async16(dst + at, second ? src1 + (at - SUB) : src0 + at);
+          for (int i = 0; i < FULL; i++) cp_async16(dst + i * 512, src0 + i * 512);
+          if (REST && lane < REST) cp_async16(dst + FULL * 512, src0 + FULL * 512);
+        }
+        if (ok1) {
+#pragma unroll
+          for (int i = 0; i < FULL; i++) cp_async16(dst + SUB + i * 512, src1 + i * 512);
+          if (REST && lane < REST) cp_async16(dst + SUB + FULL * 512, src1 + FULL * 512);
         }
       }
       cp_async_commit();
@@ -383,22 +379,21 @@ __global__ void __launch_bounds__(kThreads, MINB) cache4_attn_kernel(const __gri
 #pragma unroll
           for (int e = 0; e < 4; e++) S[mt][nt][e] = 0.f;
           mma16816(S[mt][nt], mn[0], mn[1], mn[0], mn[1], z.x, z.y);
+#pragma unroll
+          for (int e = 0; e < 4; e++) S[mt][nt][e] *= 0x1p-24f;
         }
 #pragma unroll
         for (int j = 0; j < NG; j++) {
           const uint32_t x0 = kw[0][j], x1 = kw[1][j], y0 = x0 >> 8, y1 = x1 >> 8;
-          const uint32_t a0 = code_lo(x0), a1 = code_lo(x1), a2 = code_hi(x0), a3 = code_hi(x1);
-          const uint32_t b0 = code_lo(y0), b1 = code_lo(y1), b2 = code_hi(y0), b3 = code_hi(y1);
+          constexpr uint32_t lo = 0x000f000fu, hi = 0x00f000f0u;
           const float s0 = (j & 1) ? half_hi(sc[0][j / 2]) : half_lo(sc[0][j / 2]);
           const float s1 = (j & 1) ? half_hi(sc[1][j / 2]) : half_lo(sc[1][j / 2]);
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
             const uint4 q = NT == 1 ? qreg[NT == 1 ? j : 0] : sm.q.frag[nt][j][lane];
-            const float2 st = NT == 1 ? qstart[NT == 1 ? j : 0]
-                                      : *reinterpret_cast<const float2*>(&sm.q.start[nt][j][2 * c]);
-            float C[4] = {st.x, st.y, st.x, st.y};
-            mma16816(C, a0, a1, a2, a3, q.x, q.y);
-            mma16816(C, b0, b1, b2, b3, q.z, q.w);
+            float C[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(C, x0 & lo, x1 & lo, x0 & hi, x1 & hi, q.x, q.y);
+            mma16816(C, y0 & lo, y1 & lo, y0 & hi, y1 & hi, q.z, q.w);
             S[mt][nt][0] = fmaf(C[0], s0, S[mt][nt][0]);
             S[mt][nt][1] = fmaf(C[1], s0, S[mt][nt][1]);
             S[mt][nt][2] = fmaf(C[2], s1, S[mt][nt][2]);
@@ -656,11 +651,13 @@ cudaError_t launch_cache4_attn(Cache4AttnArgs a, cudaStream_t st) {
   if (a.d == 64) {
     if (rows <= 8) return go<2, 1, 4, 4>(a, st);
     if (rows <= 16) return go<2, 2, 4, 4>(a, st);
+    if (rows <= 24) return go<2, 3, 4, 3>(a, st);
     return go<2, 4, 4, 3>(a, st);
   }
   if (a.d == 128) {
     if (rows <= 8) return go<4, 1, 2, 4>(a, st);
     if (rows <= 16) return go<4, 2, 3, 3>(a, st);
+    if (rows <= 24) return go<4, 3, 3, 2>(a, st);
     return go<4, 4, 3, 2>(a, st);
   }
   if (rows <= 8) return go<8, 1, 2, 2>(a, st);
