@@ -217,8 +217,57 @@ __global__ void __launch_bounds__(kThreads, MINB) cache4_attn_kernel(const __gri
     const int see_max = max(0, rq.held - (rq.n - 1 - (tile * ROWS + rows - 1) / group));
     const int* table = a.table + r * a.table_stride;
 
-    // ---- the tile's queries
     __syncthreads();  // the last tile's readers of sm are done
+
+    // ---- this warp's steps: w, w + 4, ...; the first copies fly while the queries are prepared
+    const int last = min(s_end, (see_max + kStep - 1) / kStep);
+    uint8_t* ring = &sm.ring[w][0][0];
+    const uint32_t ring_at = sm100::smem_addr(ring);
+    int next = s_begin + w;          // step that is copied next
+    int page0 = 0, page1 = 0;        // its pages (one each 16 keys)
+    uint32_t bad = 0;                // two bits a ring slot: a page outside the cache
+    auto load_pages = [&](int s) {
+      if (s < last) {
+        const int k0 = s * kStep;
+        page0 = table[k0 >> a.page_shift];
+        page1 = k0 + 16 < rq.held ? table[(k0 + 16) >> a.page_shift] : -1;
+      }
+    };
+    auto issue = [&](int s, int slot) {
+      bad &= ~(3u << (2 * slot));
+      if (s < last) {
+        const int k0 = s * kStep, in_page = (k0 & ((1 << a.page_shift) - 1)) >> 4;
+        const bool ok0 = (unsigned)page0 < (unsigned)a.n_pages;
+        const bool ok1 = (unsigned)page1 < (unsigned)a.n_pages;
+        bad |= ((ok0 ? 0u : 1u) | (ok1 ? 0u : 2u)) << (2 * slot);
+        const uint8_t* src0 = a.cache + ((((size_t)page0 * a.Hkv + h) << (a.page_shift - 4)) + in_page) * SUB + lane * 16;
+        const uint8_t* src1 = a.cache + ((((size_t)page1 * a.Hkv + h) << (a.page_shift - 4)) +
+                                         (a.page_shift == 4 ? 0 : in_page + 1)) * SUB + lane * 16;
+        const uint32_t dst = ring_at + slot * (2 * SUB) + lane * 16;
+        // a sub-block is FULL copies of 512 bytes, and the rest by the first lanes
+        constexpr int FULL = SUB / 512, REST = SUB % 512 / 16;
+        if (ok0) {
+#pragma unroll
+          for (int i = 0; i < FULL; i++) cp_async16(dst + i * 512, src0 + i * 512);
+          if (REST && lane < REST) cp_async16(dst + FULL * 512, src0 + FULL * 512);
+        }
+        if (ok1) {
+#pragma unroll
+          for (int i = 0; i < FULL; i++) cp_async16(dst + SUB + i * 512, src1 + i * 512);
+          if (REST && lane < REST) cp_async16(dst + SUB + FULL * 512, src1 + FULL * 512);
+        }
+      }
+      cp_async_commit();
+    };
+    load_pages(next);
+#pragma unroll
+    for (int k = 0; k < ST; k++) {
+      issue(next, k);
+      next += kWarps;
+      load_pages(next);
+    }
+
+    // ---- the tile's queries
     for (int nt = w; nt < NT; nt += kWarps) {
       const int row = tile * ROWS + nt * 8 + g;  // of this lane's quad
       const bool live = row < rq.n * group;
@@ -295,53 +344,6 @@ __global__ void __launch_bounds__(kThreads, MINB) cache4_attn_kernel(const __gri
         for (int e = 0; e < 4; e++) O[i][nt][e] = 0.f;
     }
 
-    // ---- this warp's steps: w, w + 4, ...
-    const int last = min(s_end, (see_max + kStep - 1) / kStep);
-    uint8_t* ring = &sm.ring[w][0][0];
-    const uint32_t ring_at = sm100::smem_addr(ring);
-    int next = s_begin + w;          // step that is copied next
-    int page0 = 0, page1 = 0;        // its pages (one each 16 keys)
-    uint32_t bad = 0;                // two bits a ring slot: a page outside the cache
-    auto load_pages = [&](int s) {
-      if (s < last) {
-        const int k0 = s * kStep;
-        page0 = table[k0 >> a.page_shift];
-        page1 = k0 + 16 < rq.held ? table[(k0 + 16) >> a.page_shift] : -1;
-      }
-    };
-    auto issue = [&](int s, int slot) {
-      bad &= ~(3u << (2 * slot));
-      if (s < last) {
-        const int k0 = s * kStep, in_page = (k0 & ((1 << a.page_shift) - 1)) >> 4;
-        const bool ok0 = (unsigned)page0 < (unsigned)a.n_pages;
-        const bool ok1 = (unsigned)page1 < (unsigned)a.n_pages;
-        bad |= ((ok0 ? 0u : 1u) | (ok1 ? 0u : 2u)) << (2 * slot);
-        const uint8_t* src0 = a.cache + ((((size_t)page0 * a.Hkv + h) << (a.page_shift - 4)) + in_page) * SUB + lane * 16;
-        const uint8_t* src1 = a.cache + ((((size_t)page1 * a.Hkv + h) << (a.page_shift - 4)) +
-                                         (a.page_shift == 4 ? 0 : in_page + 1)) * SUB + lane * 16;
-        const uint32_t dst = ring_at + slot * (2 * SUB) + lane * 16;
-        // a sub-block is FULL copies of 512 bytes, and the rest by the first lanes
-        constexpr int FULL = SUB / 512, REST = SUB % 512 / 16;
-        if (ok0) {
-#pragma unroll
-          for (int i = 0; i < FULL; i++) cp_async16(dst + i * 512, src0 + i * 512);
-          if (REST && lane < REST) cp_async16(dst + FULL * 512, src0 + FULL * 512);
-        }
-        if (ok1) {
-#pragma unroll
-          for (int i = 0; i < FULL; i++) cp_async16(dst + SUB + i * 512, src1 + i * 512);
-          if (REST && lane < REST) cp_async16(dst + SUB + FULL * 512, src1 + FULL * 512);
-        }
-      }
-      cp_async_commit();
-    };
-    load_pages(next);
-#pragma unroll
-    for (int k = 0; k < ST; k++) {
-      issue(next, k);
-      next += kWarps;
-      load_pages(next);
-    }
     int slot = 0;
     for (int s = s_begin + w; s < last; s += kWarps) {
       cp_async_wait<ST - 1>();
@@ -655,7 +657,7 @@ cudaError_t launch_cache4_attn(Cache4AttnArgs a, cudaStream_t st) {
     return go<2, 4, 4, 3>(a, st);
   }
   if (a.d == 128) {
-    if (rows <= 8) return go<4, 1, 2, 4>(a, st);
+    if (rows <= 8) return go<4, 1, 2, 3>(a, st);
     if (rows <= 16) return go<4, 2, 3, 3>(a, st);
     if (rows <= 24) return go<4, 3, 3, 2>(a, st);
     return go<4, 4, 3, 2>(a, st);
