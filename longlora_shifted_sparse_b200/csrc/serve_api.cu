@@ -160,7 +160,9 @@ s2_status s2attn_cache4_append(const void* k, const void* v, void* cache, const 
                                void* cuda_stream) {
   if (!k || !v || !cache || !slots || !k_strides || !v_strides) return S2_ERR_NULL;
   if (!dtype_ok(dtype)) return S2_ERR_DTYPE;
-  if (T <= 0 || H_kv <= 0 || H_kv > 65535 || !cache_ok(n_pages, page_size)) return S2_ERR_SHAPE;
+  if (T <= 0 || H_kv <= 0 || H_kv > 65535 || (long long)T * H_kv > 0x7fffffffLL ||
+      !cache_ok(n_pages, page_size))
+    return S2_ERR_SHAPE;
   if (!headdim32_ok(d)) return S2_ERR_HEADDIM;
   const int shift = page_shift(page_size);
   if (shift < 0) return S2_ERR_ARG;
@@ -185,7 +187,9 @@ s2_status s2attn_cache4_read(const void* cache, const int* slots, void* k, void*
                              void* cuda_stream) {
   if (!k || !v || !cache || !slots) return S2_ERR_NULL;
   if (!dtype_ok(dtype)) return S2_ERR_DTYPE;
-  if (T <= 0 || H_kv <= 0 || H_kv > 65535 || !cache_ok(n_pages, page_size)) return S2_ERR_SHAPE;
+  if (T <= 0 || H_kv <= 0 || H_kv > 65535 || (long long)T * H_kv > 0x7fffffffLL ||
+      !cache_ok(n_pages, page_size))
+    return S2_ERR_SHAPE;
   if (!headdim32_ok(d)) return S2_ERR_HEADDIM;
   const int shift = page_shift(page_size);
   if (shift < 0) return S2_ERR_ARG;
