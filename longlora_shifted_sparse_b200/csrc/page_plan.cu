@@ -73,6 +73,7 @@ __device__ inline PlanSizes plan_sizes(const PlanArgs& a, int r, int& cached) {
   return s;
 }
 
+template <int E>
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_constant__ PlanArgs a) {
   extern __shared__ int sh[];
   __shared__ long long warp_sums[kPlanThreads / 32];
@@ -123,23 +124,46 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     a.counts[0] = free_count - taken_max;
     a.counts[1] = left_out;
   }
+  // E tokens a thread: one search, and one page number as long as they share a page
   const int stride = gridDim.x * kPlanThreads;
-  for (int t = blockIdx.x * kPlanThreads + threadIdx.x; t < a.T; t += stride) {
-    int pos = 0, slot = -1;
-    if (t < T) {
-      const int r = find_request(tok, a.R, t);
+  const bool wide = (((uintptr_t)a.positions | (uintptr_t)a.slots) & 15) == 0;
+  for (long long t0 = (long long)E * (blockIdx.x * kPlanThreads + threadIdx.x); t0 < a.T; t0 += (long long)E * stride) {
+    int r = t0 < T ? find_request(tok, a.R, (int)t0) : 0, last = -1, base = 0;
+    int pos[E], slot[E];
+#pragma unroll
+    for (int e = 0; e < E; e++) {
+      const int t = (int)t0 + e;
+      pos[e] = 0;
+      slot[e] = -1;
+      if (t0 + e >= min(T, a.T)) continue;
+      while (t >= tok[r + 1]) {
+        r++;
+        last = -1;
+      }
       const int c = a.cached[r];
-      pos = (int)((unsigned)c + (unsigned)(t - tok[r]));
-      if (page[r] >= 0) {
-        const int col = pos >> a.page_shift;
+      pos[e] = (int)((unsigned)c + (unsigned)(t - tok[r]));
+      if (page[r] < 0) continue;
+      const int col = pos[e] >> a.page_shift;
+      if (col != last) {
         const int held = (c + (1 << a.page_shift) - 1) >> a.page_shift;
         const int p = col < held ? a.table[r * a.table_stride + col]
                                  : a.free_pages[free_count - 1 - (page[r] + col - held)];
-        slot = (int)((unsigned)p << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+        base = (int)((unsigned)p << a.page_shift);
+        last = col;
       }
+      slot[e] = base + (pos[e] & ((1 << a.page_shift) - 1));
     }
-    a.positions[t] = pos;
-    a.slots[t] = slot;
+    if (E == 4 && wide && t0 + 4 <= a.T) {
+      *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[E > 1], pos[E > 2 ? 2 : 0], pos[E - 1]);
+      *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[E > 1], slot[E > 2 ? 2 : 0], slot[E - 1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; e++)
+        if (t0 + e < a.T) {
+          a.positions[t0 + e] = pos[e];
+          a.slots[t0 + e] = slot[e];
+        }
+    }
   }
   // the pages' places in the table: a lane's run of the pages taken
   const int take = taken_max;
@@ -159,9 +183,15 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
 
 cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t st) {
   const size_t smem = (2 * a.R + 1) * sizeof(int);
-  int blocks = (a.T + kPlanThreads - 1) / kPlanThreads;
-  blocks = blocks < 1 ? 1 : blocks > 148 ? 148 : blocks;
-  page_plan_kernel<<<blocks, kPlanThreads, smem, st>>>(a);
+  // Few tokens: one a thread, for latency (64 requests of a token each: 5.4 us against 8.2 with four).
+  // Many: four (509 prompts, 1 M tokens: 12.3 us; one a thread on a CTA per SM took 32).
+  const bool few = a.T <= 148 * kPlanThreads;
+  const long long per = few ? kPlanThreads : 4 * kPlanThreads, need = (a.T + per - 1) / per;
+  const int blocks = (int)(need < 1 ? 1 : need > 148 * 8 ? 148 * 8 : need);
+  if (few)
+    page_plan_kernel<1><<<blocks, kPlanThreads, smem, st>>>(a);
+  else
+    page_plan_kernel<4><<<blocks, kPlanThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 

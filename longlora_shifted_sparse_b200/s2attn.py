@@ -512,12 +512,16 @@ def page_plan(cached_lens, new_lens, free_pages, free_count, block_table, page_s
     c, n = _ints(cached_lens, "cached_lens", dev, (R,)), _ints(new_lens, "new_lens", dev, (R,))
     f, fc = _ints(free_pages, "free_pages", dev), _ints(free_count, "free_count", dev, (1,))
     cols, stride = _table(block_table, dev, R)
-    out = torch.empty(2 * R + 3 + 2 * max_tokens, dtype=_i32, device=dev)
-    p, b = out.data_ptr(), 4 * (2 * R + 1)
-    _call(dev, s2attn_page_plan, c, n, f, fc, block_table.data_ptr(), p, p + 4 * (R + 1), p + b,
-          p + b + 4 * max_tokens, p + b + 8 * max_tokens, R, max_tokens, free_pages.numel(), cols,
-          stride, page_size)
-    return PagePlan(*out.split_with_sizes((R + 1, R, max_tokens, max_tokens, 1, 1)))
+    rows = (max_tokens + 3) & ~3   # positions and slots on 16 bytes
+    out = torch.empty(2 * rows + 2 * R + 3, dtype=_i32, device=dev)
+    p = out.data_ptr()
+    cu = p + 8 * rows
+    _call(dev, s2attn_page_plan, c, n, f, fc, block_table.data_ptr(), cu, cu + 4 * (R + 1), p, p + 4 * rows,
+          cu + 4 * (2 * R + 1), R, max_tokens, free_pages.numel(), cols, stride, page_size)
+    pos, slots, cu, lens, left, out_of = out.split_with_sizes((rows, rows, R + 1, R, 1, 1))
+    if rows != max_tokens:
+        pos, slots = pos[:max_tokens], slots[:max_tokens]
+    return PagePlan(cu, lens, pos, slots, left, out_of)
 
 
 def cache4(n_pages: int, page_size: int, Hkv: int, d: int, device="cuda"):
