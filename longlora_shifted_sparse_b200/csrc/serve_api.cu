@@ -50,8 +50,16 @@ constexpr size_t kCache4WsBytes =
 
 // Tensor instructions: bf16 and a head dim that is a whole number of their wide loads.
 bool cache4_mma(int d, int dt) { return dt == S2_BF16 && (d == 64 || d == 128 || d == 256); }
-// Many rows of a kv head: tiles of 256 rows rather than of 8 to 32.
-bool cache4_many(int d, long long rows) { return (d == 64 || d == 128) && rows > 64; }
+// Tiles of 256 query rows on tcgen05, or of 8 to 32 on mma.sync? The first dequantise a key once for
+// many rows; the second start sooner. `rows`: of a request and kv head; `pairs`: rows times keys of
+// the whole call, at most what the block table's width allows. us, mma.sync / tcgen05, d = 128:
+//   1 request, 64 heads on 8, 1024 keys:  64 rows 23 / 28, 128 rows 21 / 29, 512 rows 38 / 37
+//   1 request, 64 heads on 8, 4096 keys:  32 rows 28 / 29,  64 rows 34 / 31, 512 rows 68 / 41
+//   8 requests, 32 heads on 32, 4096 keys: 32 rows 97 / 123, 64 rows 145 / 130, 512 rows 763 / 259
+//   1 request, 64 heads on 8, 16384 keys: 64 rows 58 / 49, 512 rows 187 / 76
+bool cache4_many(int d, long long rows, double pairs) {
+  return (d == 64 || d == 128) && rows >= 64 && pairs >= 3.0 * (1 << 20);
+}
 
 }  // namespace
 }  // namespace s2
@@ -243,7 +251,8 @@ s2_status s2attn_cache4_attn(const void* q, const void* cache, const int* block_
     a.counters = reinterpret_cast<unsigned*>(ws + kAtCounters);
     a.joins = reinterpret_cast<int4*>(ws + kAtJoins);
     a.part_o = reinterpret_cast<float*>(ws + kAtParts);
-    if (cache4_many(d, (long long)max_new * (H_q / H_kv))) {
+    const long long rows = (long long)max_new * (H_q / H_kv);
+    if (cache4_many(d, rows, (double)R * H_kv * rows * ((long long)max_pages << shift))) {
       a.part_ml = a.part_o + kTcPartsO;
       return to_status(timed_launch(kCache4Tc, s, [&] { return launch_cache4_tc(a, s); }));
     }

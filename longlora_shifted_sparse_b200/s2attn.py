@@ -352,6 +352,11 @@ def _table(t, device, R):
     return shape[1], max(t.stride(0), shape[1])
 
 
+def _dense_like(x):
+    """An uninitialised dense tensor of x's shape (empty_like is the quicker call, but keeps strides)."""
+    return _torch.empty_like(x) if x.is_contiguous() else _torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
 @functools.lru_cache(maxsize=512)
 def _strides(*s):
     return (_ll * len(s))(*s)
@@ -407,7 +412,7 @@ def _rope_launch(q, k, positions, freqs, layout, mscale, inverse, in_place):
     _need(freqs.dim() == 1 and freqs.is_contiguous(), "freqs must be one dense row")
     _need(dev == positions.device == freqs.device, "q, positions and freqs must share a device")
     q4, qst = _rope_rows(q, "q")
-    out = q if in_place else torch.empty(shape, dtype=q.dtype, device=dev)
+    out = q if in_place else _dense_like(q)
     kp = kop = kst = kout = None
     Hkv = 0
     same = q4 is q
@@ -418,7 +423,7 @@ def _rope_launch(q, k, positions, freqs, layout, mscale, inverse, in_place):
               "q %s and k %s must share all but heads" % (tuple(shape), tuple(kshape)))
         k4, kst = _rope_rows(k, "k")
         same = same and k4 is k
-        kout = k if in_place else torch.empty(kshape, dtype=k.dtype, device=dev)
+        kout = k if in_place else _dense_like(k)
         Hkv, kp, kop = kshape[-2], k4.data_ptr(), kout.data_ptr()
     if in_place:
         _need(same, "in place needs dense, 16-byte aligned channels")
@@ -610,7 +615,7 @@ def cache4_attention(q, cache, block_table, lens, cu_new, max_new: int, scale=No
     cols, stride = _table(block_table, dev, R)
     q, qs = _cache4_rows(q)
     if out is None:
-        out = _torch.empty(shape, dtype=q.dtype, device=dev)
+        out = _dense_like(q)
     else:
         _need(out.shape == shape and out.dtype is q.dtype and out.device == dev and
               out.is_contiguous(), "out must be a dense tensor like q")
