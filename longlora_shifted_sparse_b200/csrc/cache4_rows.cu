@@ -1,7 +1,7 @@
 // Rows of the 4-bit cache: append (quantise k, v into their slots) and read (the values that
 // slots hold).
 //
-// A group of 32 channels of a token's head is held as fp16 scale = (max - min) / 15 and fp16
+// A group of 32 channels of a token's head is held as fp16 scale = (max - min) * (1 / 15) and fp16
 // minimum, and codes rint((x - min) / scale) within 0..15, all in IEEE fp32 with the two
 // parameters as rounded, so that their rounding costs range at the ends and no bias. Inputs
 // are first limited to fp16's range. A NaN or infinity in the k or v of a token's head
@@ -123,10 +123,8 @@ __global__ void __launch_bounds__(kRowThreads) cache4_append_kernel(const __grid
       __ballot_sync(0xffffffffu, !(fabsf(ex.x) <= 3.402823466e38f && fabsf(ex.y) <= 3.402823466e38f));
   const bool bad = (bads >> (team * TEAM)) & ((2u << (TEAM - 1)) - 1u);
   const float lo = fminf(fmaxf(ex.x, -65504.f), 65504.f), hi = fminf(fmaxf(ex.y, -65504.f), 65504.f);
-  // (hi - lo) / 15, correctly rounded: a product and a step with its residual (tried for every mantissa)
-  const float range = __fsub_rn(hi, lo), part = range * 0.0666666701f;
   __half low = __float2half_rn(lo);
-  __half scale = __float2half_rn(fmaf(fmaf(-15.f, part, range), 0.0666666701f, part));
+  __half scale = __float2half_rn(__fmul_rn(__fsub_rn(hi, lo), 0.0666666701f));  // 1 / 15
   float s = __half2float(scale);
   const float m = __half2float(low);
   if (fmaf(15.f, s, m) >= 65520.f) {  // would round to infinity in fp16

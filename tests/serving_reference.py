@@ -35,7 +35,7 @@ def quantised(x):
     """The value in 64 bits that the cache holds of finite x [T, H, d], and the groups' scales."""
     g = x.float().clamp(-65504, 65504).unflatten(-1, (-1, 32))
     low, high = g.amin(-1, keepdim=True), g.amax(-1, keepdim=True)
-    scale, low = ((high - low) / 15).half(), low.half().float()
+    scale, low = ((high - low) * (1 / 15)).half(), low.half().float()
     # a top value that would round beyond fp16 (65504 + half a step) takes the next smaller scale
     scale = torch.where(scale.double() * 15 + low.double() >= 65520, (scale.view(torch.int16) - 1).view(torch.float16), scale).float()
     safe = torch.where(scale > 0, scale, torch.ones_like(scale))

@@ -207,6 +207,19 @@ def test_codes_at_borders(s2):
             assert ((got.double() - want).abs() <= 2.0 ** -23 * want.abs() + 1e-30).all()
 
 
+@pytest.mark.parametrize("d,dtype", [(128, F32), (96, F32), (128, BF16)])
+def test_codes_of_many_groups(s2, d, dtype):
+    """Every scale, minimum and code of many groups: the values held are the format's, to the rounding of one product and sum."""
+    T, H, P = 5000, 2, 64
+    k, v = normal(1, T, H, d, dtype=dtype), normal(2, T, H, d, dtype=dtype) * torch.logspace(-3, 3, T, device="cuda").view(T, 1, 1).to(dtype)
+    cache = s2.cache4(T // P + 1, P, H, d)
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    s2.cache4_append(k, v, cache, slots)
+    for x, got in zip((k, v), s2.cache4_read(cache, slots, F32)):
+        want = ref.quantised(x)[0]
+        assert ((got.double() - want).abs() <= 2.0 ** -23 * want.abs() + 1e-30).all()
+
+
 @pytest.mark.parametrize("T_extra", [0, 1, 2, 3])
 def test_large_plans(s2, T_extra):
     g = torch.Generator().manual_seed(3)
