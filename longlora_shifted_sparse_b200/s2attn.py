@@ -300,20 +300,42 @@ def s2_attention(q, k, v, G: int, pi_scale: float, rope_base: float = 10000.0,
 #
 # Calls on tensors of another device than the current one make that device current for the
 # launch; work goes to that device's current stream. These calls run once per layer and token, so
-# their host time counts: torch's names are looked up once, checks are one expression each on
-# the way that succeeds, and stride arrays are kept by value.
+# their host time counts: the plain case (tensors of the current device, in the layouts that the
+# library takes) goes from tensors to the C ABI in one compiled call (csrc/serve_calls.cpp), which
+# leaves every other case, and what to say about it, to the code here.
 
+CALLS_PATH = os.path.join(_HERE, "_serve_calls.so")
 _torch = None
 
 
 def _lazy():
-    """torch, imported on the first call, with the names that every call needs."""
-    global _torch, _device_now, _raw_stream, _i32, _DTYPES
+    """torch and the compiled calls, imported on the first call, with the names that every call needs."""
+    global _torch, _calls, _device_now, _raw_stream, _i32, _DTYPES
     import torch
+    if not os.path.exists(CALLS_PATH):
+        raise ImportError("_serve_calls.so is not built (expected at %s); build it with "
+                          "`python -m longlora_shifted_sparse_b200.build`" % CALLS_PATH)
+    from importlib import machinery, util
+    spec = util.spec_from_file_location("_serve_calls", CALLS_PATH,
+                                        loader=machinery.ExtensionFileLoader("_serve_calls", CALLS_PATH))
+    _calls = util.module_from_spec(spec)
+    spec.loader.exec_module(_calls)
     _device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _i32, _DTYPES = torch.int32, {torch.bfloat16: S2_BF16, torch.float32: S2_FP32}
     _torch = torch
     return torch
+
+
+def _plain(call, *args):
+    """What a compiled call returns: outputs, or None where the case is not the plain one."""
+    if _torch is None:
+        _lazy()
+    if not args[0].is_cuda:   # (before any CUDA call: there may be no device)
+        return None
+    out = getattr(_calls, call)(*args)
+    if type(out) is int and out:
+        raise S2Error(out)
+    return out
 
 
 def _call(device, fn, *args) -> None:
@@ -387,6 +409,10 @@ def _rope_rows(x, name):
 
 
 def _rope_launch(q, k, positions, freqs, layout, mscale, inverse, in_place):
+    if not in_place:
+        out = _plain("rope", q, k, positions, freqs, layout == "half", mscale, inverse)
+        if out is not None:
+            return out
     torch = _torch or _lazy()
     dt, dev, shape = _DTYPES.get(q.dtype), q.device, q.shape
     if dt is None:
@@ -512,7 +538,10 @@ def page_plan(cached_lens, new_lens, free_pages, free_count, block_table, page_s
     in rows that no request owns), free_count [1] (what is left) and left_out [1]: the number
     of requests that did not fit (too long for the table or for max_tokens, or no pages left),
     whose slots are -1 and whose lengths stay."""
-    torch = _torch or _lazy()
+    out = _plain("page_plan", cached_lens, new_lens, free_pages, free_count, block_table, page_size, max_tokens)
+    if out is not None:
+        return tuple.__new__(PagePlan, out)
+    torch = _torch
     dev, R = cached_lens.device, cached_lens.numel()
     c, n = _ints(cached_lens, "cached_lens", dev, (R,)), _ints(new_lens, "new_lens", dev, (R,))
     f, fc = _ints(free_pages, "free_pages", dev), _ints(free_count, "free_count", dev, (1,))
@@ -558,6 +587,8 @@ def _cache4_rows(x):
 def cache4_append(k, v, cache, slots) -> None:
     """Stores k, v [T, Hkv, d] in the cache's slots (int32 [T]; rows with a negative slot, or one
     beyond the cache, are skipped; the others must differ)."""
+    if _plain("append", k, v, cache, slots) is not None:
+        return
     n_pages, P, Hkv, d = _cache4_shape(cache)
     dev, shape = cache.device, k.shape
     _need(len(shape) == 3 and shape == v.shape and shape[1] == Hkv and shape[2] == d,
@@ -576,6 +607,9 @@ def cache4_append(k, v, cache, slots) -> None:
 def cache4_read(cache, slots, dtype=None):
     """(k, v) [T, Hkv, d] that the slots (int32 [T]) hold, in bfloat16 or float32; slots outside
     the cache give zeros."""
+    out = _plain("read", cache, slots, S2_BF16 if dtype is None else _DTYPES.get(dtype, -1)) if _torch or _lazy() else None
+    if out is not None:
+        return out
     n_pages, P, Hkv, d = _cache4_shape(cache)
     dev, T = cache.device, slots.numel()
     at = _ints(slots, "slots", dev, (T,))
@@ -605,6 +639,11 @@ def cache4_attention(q, cache, block_table, lens, cu_new, max_new: int, scale=No
     by default. ws: ``cache4_workspace``, made anew where it is None. Returns o [T, Hq, d]
     (out, if given, whose rows that no request owns stay as they were), or (o, lse) with lse
     [Hq, T]. A row that sees no key gets 0 and -inf."""
+    if ws is None:
+        ws = cache4_workspace(q.device)
+    plain = _plain("attention", q, cache, block_table, lens, cu_new, max_new, scale, ws, out, return_lse)
+    if plain is not None:
+        return plain
     n_pages, P, Hkv, d = _cache4_shape(cache)
     dev, shape = cache.device, q.shape
     _need(len(shape) == 3 and shape[2] == d and q.device == dev,
@@ -620,8 +659,6 @@ def cache4_attention(q, cache, block_table, lens, cu_new, max_new: int, scale=No
         _need(out.shape == shape and out.dtype is q.dtype and out.device == dev and
               out.is_contiguous(), "out must be a dense tensor like q")
     lse = _torch.empty((Hq, T), dtype=_torch.float32, device=dev) if return_lse else None
-    if ws is None:
-        ws = cache4_workspace(dev)
     _need(ws.device == dev, "ws is on %s, not on %s" % (ws.device, dev))
     if T:
         _call(dev, s2attn_cache4_attn, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), ln, cu,
