@@ -284,14 +284,17 @@ S2_API s2_status s2attn_page_plan(const int* cached_lens, const int* new_lens,
 /* The 4-bit cache: n_pages pages of page_size tokens for each of H_kv heads of d channels
  * (a multiple of 32 in [32, 256]), laid out [n_pages][H_kv][page_size / 16][20 d bytes]. A
  * value is minimum + scale * code (0..15), one fp16 scale and minimum per 32 channels of a
- * token's head: 5 bits a value. Bytes, or 0 for arguments that the calls would reject. Fewer
- * than 2^31 slots; 16-byte aligned; its contents need no initialisation. */
+ * token's head: 5 bits a value. scale = (maximum - minimum) * (1 / 15) and code =
+ * rint((x - minimum) / scale) in fp32, with both parameters as rounded to fp16; a scale whose top
+ * value would round beyond fp16 is taken one step smaller. Bytes, or 0 for arguments that the
+ * calls would reject. Fewer than 2^31 slots, H_kv at most 65535; 16-byte aligned; its contents
+ * need no initialisation. */
 S2_API size_t s2attn_cache4_bytes(int n_pages, int page_size, int H_kv, int d);
 
 /* Stores k, v [T][H_kv][d] (strides of token and head in elements, multiples of 16 bytes) in
  * the cache's slots[0 .. T-1]. Rows whose slot is negative or beyond the cache are skipped.
- * Slots of one call must differ: rows that share one leave it undefined. Values are limited
- * to +-65504. A NaN or infinity in the k or v of a token's head makes that (token, head) NaN
+ * Slots of one call must differ: rows that share one leave it undefined. T * H_kv below 2^31.
+ * Values are limited to +-65504. A NaN or infinity in the k or v of a token's head makes that (token, head) NaN
  * for every query that attends to it, and leaves the others alone. */
 S2_API s2_status s2attn_cache4_append(const void* k, const void* v, void* cache, const int* slots,
                                       int T, int H_kv, int d, int n_pages, int page_size,
@@ -305,7 +308,10 @@ S2_API s2_status s2attn_cache4_read(const void* cache, const int* slots, void* k
                                     void* cuda_stream);
 
 /* Bytes of workspace of s2attn_cache4_attn, for every shape. It must be zero before its first
- * use; each call leaves it ready for the next. A workspace serves one call at a time. */
+ * use; each call leaves it ready for the next. A workspace serves one call at a time (two graphs
+ * that were captured with the same one must not run at once). The waits of the kernel for many
+ * rows are bounded: when one expires the outputs are undefined and
+ * s2attn_device_status(workspace, ...) reports S2_ERR_DEVICE_TIMEOUT. */
 S2_API size_t s2attn_cache4_workspace_bytes(void);
 
 /* Attention over the cache: o[t] = softmax(q[t] k^T * scale) v over request r's slots, for its
@@ -315,9 +321,11 @@ S2_API size_t s2attn_cache4_workspace_bytes(void);
  * before. Query head h uses kv head h / (H_q / H_kv). o is dense [T][H_q][d]; lse, if not
  * NULL, is [H_q][T] float32. A row that sees no key gets o = 0 and lse = -inf; rows that no
  * request owns stay as they were. max_new: the largest number of rows of a request, from
- * which the kernel's tile is chosen (another value costs time, not correctness). A page
- * number outside the cache among those a row attends to makes that row NaN; lens beyond
- * max_pages * page_size counts as that much. */
+ * which the kernel's tile is chosen (another value costs time, not correctness); so is it from
+ * R and max_pages, which bound the work. A page number outside the cache among those a row attends
+ * to makes that row NaN; lens beyond max_pages * page_size (at most 2^31 - 256) counts as that
+ * much. o must not overlap q. bf16 calls with d = 64, 128 or 256 form scores from the codes in
+ * fp32 and hold probabilities and v (for many rows k too) in fp16; the others are fp32 throughout. */
 S2_API s2_status s2attn_cache4_attn(const void* q, const void* cache, const int* block_table,
                                     const int* lens, const int* cu_new, void* o, float* lse,
                                     int R, int T, int H_q, int H_kv, int d, int n_pages,

@@ -504,7 +504,9 @@ def rope(q, k, positions, freqs, layout: str = "interleaved", mscale: float = 1.
     the rotated channels, the first 2 * len(freqs); the rest pass through. layout: pair i is
     channels (2i, 2i+1) ("interleaved", as in the attention calls) or (i, i + half)
     ("half"). mscale multiplies the rotated channels. Differentiable in q and k;
-    in_place=True overwrites them instead and has no gradient."""
+    in_place=True overwrites them instead and has no gradient. (To capture a training step into a
+    graph, drop eager graphs of the same leaves first: torch's accumulation nodes keep the stream
+    that they were made on.)"""
     if layout not in ROPE_LAYOUTS:
         raise ValueError("layout must be one of %s, got %r" % (sorted(ROPE_LAYOUTS), layout))
     grad = (q.requires_grad or (k is not None and k.requires_grad)) and (_torch or _lazy()).is_grad_enabled()
@@ -638,7 +640,8 @@ def cache4_attention(q, cache, block_table, lens, cu_new, max_new: int, scale=No
     of rows of a request (known to the caller; it picks the kernel's tile). scale: 1 / sqrt(d)
     by default. ws: ``cache4_workspace``, made anew where it is None. Returns o [T, Hq, d]
     (out, if given, whose rows that no request owns stay as they were), or (o, lse) with lse
-    [Hq, T]. A row that sees no key gets 0 and -inf."""
+    [Hq, T]. A row that sees no key gets 0 and -inf. ``device_status(ws)`` reads whether a wait inside
+    the call expired."""
     if ws is None:
         ws = cache4_workspace(q.device)
     plain = _plain("attention", q, cache, block_table, lens, cu_new, max_new, scale, ws, out, return_lse)
