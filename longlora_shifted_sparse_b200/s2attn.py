@@ -482,16 +482,17 @@ def _make_rope_function():
         """Autograd wrapper: the gradient is the same rotation the other way round."""
 
         @staticmethod
-        def forward(ctx, q, k, positions, freqs, layout, mscale):
+        def forward(ctx, q, k, positions, freqs, layout, mscale, inverse):
             ctx.save_for_backward(positions, freqs)
-            ctx.args = (layout, mscale)
-            return _rope_launch(q, k, positions, freqs, layout, mscale, False, False)
+            ctx.args = (layout, mscale, not inverse)
+            return _rope_launch(q, k, positions, freqs, layout, mscale, inverse, False)
 
         @staticmethod
         def backward(ctx, dq, dk):
-            positions, freqs = ctx.saved_tensors
-            dq, dk = _rope_launch(dq, dk, positions, freqs, *ctx.args, True, False)
-            return dq, dk, None, None, None, None
+            call = (dq, dk, *ctx.saved_tensors, *ctx.args)
+            # (the launch itself unless a gradient of the gradient may be asked for)
+            dq, dk = RopeFunction.apply(*call) if torch.is_grad_enabled() else _rope_launch(*call, False)
+            return dq, dk, None, None, None, None, None
 
     return RopeFunction
 
@@ -516,7 +517,7 @@ def rope(q, k, positions, freqs, layout: str = "interleaved", mscale: float = 1.
     global _rope_fn
     if _rope_fn is None:
         _rope_fn = _make_rope_function()
-    return _rope_fn.apply(q, k, positions, freqs, layout, mscale)
+    return _rope_fn.apply(q, k, positions, freqs, layout, mscale, False)
 
 
 class PagePlan(NamedTuple):

@@ -150,3 +150,53 @@ def test_on_a_stream_of_its_own(s2):
         o = s2.cache4_attention(x, *args, ws=ws)
     side.synchronize()
     assert torch.equal(o, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+def test_rope_gradients_of_parts(s2, both, layout):
+    """Gradients where only one output is used, through sums, for q alone, and of the gradient itself."""
+    f, pos = s2.rope_freqs(32, pi_scale=2.0), torch.arange(7, 12, device="cuda")
+    q, k, w = (normal(s, 2, 5, 3, 48).requires_grad_() for s in (1, 2, 3))
+    turn = lambda x, **kw: s2.rope(x, None, pos, f, layout, 1.5, **kw)[0]  # noqa: E731
+
+    def parts():
+        y, z = s2.rope(q, k, pos, f, layout, 1.5)
+        gq, gk = torch.autograd.grad((y * w).sum() + z.sum(), (q, k), create_graph=True)
+        only_k = torch.autograd.grad(s2.rope(q, k, pos, f, layout, 1.5)[1].square().sum(), (q, k), allow_unused=True)
+        (second,) = torch.autograd.grad((gq * gq.detach()).sum(), w)
+        return gq.detach(), gk, only_k[1], second, only_k[0] is None or not only_k[0].any()
+
+    for gq, gk, only_k, second, unused in both(parts):
+        assert unused
+        # the map is linear, R^T R = 1.5^2 on the rotated channels and 1 beyond: each gradient by the map itself
+        with torch.no_grad():
+            probe = normal(9, 2, 5, 3, 48)
+            assert abs((turn(probe) * w).sum() - (probe * gq).sum()) <= 1e-3
+            assert abs(turn(probe).sum() - (probe * gk).sum()) <= 1e-3
+            scale = torch.ones(48, device="cuda")
+            scale[:32] = 1.5 ** 2
+            assert torch.allclose(only_k, 2 * k * scale, rtol=1e-5, atol=1e-5)
+            assert torch.allclose(second, w * scale, rtol=1e-5, atol=1e-5)
+
+
+@pytest.mark.gpu
+def test_captured_rope_step(s2):
+    q, f, pos = normal(1, 2, 9, 4, 64, dtype=BF16).requires_grad_(), s2.rope_freqs(64), torch.arange(9, device="cuda")
+    dy = normal(2, 2, 9, 4, 64, dtype=BF16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(s2.rope(q, None, pos, f)[0], q, dy)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = s2.rope(q, None, pos, f)[0]
+        (dq,) = torch.autograd.grad(y, q, dy)
+    for s in (3, 4):
+        with torch.no_grad():
+            q.copy_(normal(s, 2, 9, 4, 64, dtype=BF16))
+            dy.copy_(normal(s + 5, 2, 9, 4, 64, dtype=BF16))
+        graph.replay()
+        z = s2.rope(q, None, pos, f)[0]
+        assert torch.equal(y, z) and torch.equal(dq, torch.autograd.grad(z, q, dy)[0])
