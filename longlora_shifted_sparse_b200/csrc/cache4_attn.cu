@@ -21,11 +21,20 @@
 // probabilities: both well below the output's bf16. Maxima, sums and accumulators are fp32.
 //
 // Work is steps of 32 keys of a (request, kv head, tile). All steps of the call lie on one line
-// and each CTA takes an equal run of them, whatever the requests' lengths; its four warps
-// take every fourth step, each with its own ring of cp.async copies, and meet only at the
-// end of a tile. A tile that several CTAs share is joined by the last of them to arrive, in the
-// order of the runs, so that the bits do not depend on timing.
+// and each CTA takes an equal run of them, whatever the requests' lengths, or, of short calls, one
+// equal part of one tile; its four warps take every fourth step, each with its own ring of cp.async
+// copies, and meet only at the end of a tile. A tile that several CTAs share is joined by the last of
+// them to arrive, in the order of the runs, so that the bits do not depend on timing.
+//
+// Measured (B200): 102400 tokens, 32 heads on 32 of 128: 119 us, 524 MB, 4.4 TB/s; 24 requests of up to 32768, 64
+// on 8 of 128: 146 us, 653 MB, 4.5 TB/s. The copies alone take 90 us of the 119, the loop without v 92,
+// without three quarters of k 105: what is left over is the extraction of the codes, two logic or
+// permute operations for a code pair on a pipe that takes one every other cycle. Three CTAs an SM
+// with 168 registers did better than four with 128 (127 us); a maximum that is kept (123), shifts
+// as multiplications (128) and e4m3 operands for k's codes (142) did worse.
 #include <math.h>
+
+#include <type_traits>
 
 #include "cache4.cuh"
 #include "common.cuh"
@@ -36,10 +45,12 @@ namespace s2 {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kStep = 32;  // keys of a step
+constexpr int kTries = 4, kCutChunk = 128;
+__device__ constexpr int kMore[kTries] = {0, 2, 5, 10};  // steps
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -144,6 +155,7 @@ struct Smem {
   float m[kWarps][NT * 8], l[kWarps][NT * 8];
   Queries<NG, NT> q;
   long long scan[kWarps];
+  int tries[kWarps][kTries];
   long long find_base;
   int find_r, last;
 };
@@ -156,57 +168,154 @@ __global__ void __launch_bounds__(kThreads, MINB) cache4_attn_kernel(const __gri
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const int group = a.Hq / a.Hkv;
 
-  // ---- this CTA's run of steps, and the request that it starts in
-  const int per = (a.R + kThreads - 1) / kThreads;
-  const int r_lo = min((int)threadIdx.x * per, a.R), r_hi = min(r_lo + per, a.R);
-  long long mine = 0;
-  for (int r = r_lo; r < r_hi; r++) {
-    const Request q = request(a, r, ROWS);
-    mine += (long long)a.Hkv * q.tiles * q.steps;
-  }
-  long long before = mine;
+  // ---- this CTA's run of steps, and the request that it starts in. Up to 32 requests are a lane each,
+  // in every warp for itself; more are spread over the threads, and the warps' sums meet in shared memory.
+  // (One request needs no sums.)
+  const bool alone = a.R <= 32, one = a.R == 1;
+  const int per = alone ? 1 : (a.R + kThreads - 1) / kThreads;
+  const int r_lo = one ? 0 : min((alone ? lane : (int)threadIdx.x) * per, a.R), r_hi = min(r_lo + per, a.R);
+  auto upto = [&](auto x) {  // sum over the lanes up to this one
+    if (one) return x;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += y;
-  }
-  if (lane == 31) sm.scan[w] = before;
-  __syncthreads();
-  long long total = 0;
-  before -= mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const auto y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  const int cta = blockIdx.x, grid = gridDim.x;
+  long long chunk = a.min_chunk, mine = 0, before = 0, total = 0;
+  int more = -1, ctas = 0, my_parts = 0, parts_before = 0;
+  // Cuts every tile into equal parts of at most chunk + kMore[k] steps, k = 0 .. N - 1, and takes the first k
+  // whose parts fit the grid.
+  auto cut = [&](auto tries) {
+    constexpr int N = decltype(tries)::value, W = (N + 1) / 2;
+    int parts[2 * W], sums[2 * W];
 #pragma unroll
-  for (int i = 0; i < kWarps; i++) {
-    if (i < w) before += sm.scan[i];
-    total += sm.scan[i];
-  }
-  const long long chunk = max((total + gridDim.x - 1) / (long long)gridDim.x, (long long)a.min_chunk);
-  const long long run0 = blockIdx.x * chunk, run1 = min(run0 + chunk, total);
-  if (run0 >= total) return;
-  if (before <= run0 && run0 < before + mine) {
-    long long at = before;
+    for (int k = 0; k < 2 * W; k++) parts[k] = 0;
     for (int r = r_lo; r < r_hi; r++) {
       const Request q = request(a, r, ROWS);
-      const long long size = (long long)a.Hkv * q.tiles * q.steps;
-      if (run0 < at + size) {
-        sm.find_r = r;
-        sm.find_base = at;
-        break;
+      const long long units = (long long)a.Hkv * q.tiles;
+#pragma unroll
+      for (int k = 0; k < N; k++) {
+        const unsigned len = (unsigned)chunk + kMore[k];
+        parts[k] = (int)min(parts[k] + units * ((q.steps + len - 1) / len), (long long)kCache4MaxCtas + 1);
       }
+    }
+#pragma unroll
+    for (int k = 0; k < W; k++) {  // two sums in a word: 32 lanes of at most kCache4MaxCtas + 1
+      static_assert(32 * (kCache4MaxCtas + 1) < 1 << 15, "");
+      const int both = upto(parts[2 * k] | parts[2 * k + 1] << 16);
+      sums[2 * k] = both & 0xffff;
+      sums[2 * k + 1] = both >> 16;
+    }
+    if (!alone) {
+      if (lane == 31)
+#pragma unroll
+        for (int k = 0; k < N; k++) sm.tries[w][k] = sums[k];
+      __syncthreads();
+    }
+#pragma unroll
+    for (int k = N - 1; k >= 0; k--) {
+      int all = 0, earlier = 0;
+      if (alone) {
+        all = __shfl_sync(0xffffffffu, sums[k], 31);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kWarps; i++) {
+          if (i < w) earlier += sm.tries[i][k];
+          all += sm.tries[i][k];
+        }
+      }
+      if (all <= grid) {
+        more = kMore[k];
+        ctas = all;
+        my_parts = parts[k];
+        parts_before = earlier + sums[k] - parts[k];
+      }
+    }
+  };
+  // A grid with room for all parts of min_chunk steps that the table's width allows needs no more than that.
+  if (a.roomy) cut(std::integral_constant<int, 1>{});
+  if (more < 0) {
+    for (int r = r_lo; r < r_hi; r++) {
+      const Request q = request(a, r, ROWS);
+      mine += (long long)a.Hkv * q.tiles * q.steps;
+    }
+    before = upto(mine);
+    if (alone) {
+      total = __shfl_sync(0xffffffffu, before, 31);
+    } else {
+      if (lane == 31) sm.scan[w] = before;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kWarps; i++) {
+        if (i < w) before += sm.scan[i];
+        total += sm.scan[i];
+      }
+    }
+    before -= mine;
+    chunk = max(total < (1LL << 31) - grid ? (long long)(((unsigned)total + grid - 1) / (unsigned)grid)
+                                           : (total + grid - 1) / grid,
+                (long long)a.min_chunk);
+    // Equal runs of the line. Shorter ones end where tiles end, if a few steps more than that allow it (a
+    // step is 0.4 us of a CTA): no CTA then visits two tiles, each with its queries, sums and join (5 us).
+    // 3 requests of up to 5000 keys, 32 heads on 2 of 128: 21.8 us against 26.5; 8 of 4096, 64 on 8: 18.8
+    // against 20.8; with 230 steps a CTA it is a loss.
+    if (chunk <= kCutChunk) cut(std::integral_constant<int, kTries>{});
+  }
+  const long long run0 = cta * chunk;
+  if (more >= 0 ? cta >= ctas : run0 >= total) return;
+  int found = -1;
+  long long at = more >= 0 ? parts_before : before;  // parts, or steps, of the requests before
+  const long long goal = more >= 0 ? cta : run0, ahead = more >= 0 ? my_parts : mine;
+  if (at <= goal && goal < at + ahead) {
+    for (found = r_lo;; found++) {
+      const Request q = request(a, found, ROWS);
+      const int len = (int)chunk + more;
+      const long long size = (long long)a.Hkv * q.tiles * (more >= 0 ? (q.steps + len - 1) / len : q.steps);
+      if (goal < at + size) break;
       at += size;
     }
   }
-  __syncthreads();
-  int r = sm.find_r;
-  long long base = sm.find_base;  // where request r's steps begin
-
+  int r;
+  if (alone) {
+    const int who = __ffs(__ballot_sync(0xffffffffu, found >= 0)) - 1;
+    r = __shfl_sync(0xffffffffu, found, who);
+    at = __shfl_sync(0xffffffffu, at, who);
+  } else {
+    if (found >= 0) {
+      sm.find_r = found;
+      sm.find_base = at;
+    }
+    __syncthreads();
+    r = sm.find_r;
+    at = sm.find_base;
+  }
   Request rq = request(a, r, ROWS);
-  long long pos = run0;
+  long long base, pos, run1;      // where request r's steps begin on the line; this CTA's run
+  int part_of = 0, parts_of = 0;  // its part, of how many, of a tile that is cut into equal ones
+  if (more >= 0) {
+    const int len = (int)chunk + more;
+    parts_of = (rq.steps + len - 1) / len;
+    const int part = cta - (int)at, unit = part / parts_of;
+    part_of = part - unit * parts_of;
+    base = 0;
+    const int equal = (rq.steps + parts_of - 1) / parts_of;  // at most len, so that none is empty
+    pos = (long long)unit * rq.steps + part_of * equal;
+    run1 = (long long)unit * rq.steps + min(rq.steps, (part_of + 1) * equal);
+  } else {
+    base = at;
+    pos = run0;
+    run1 = min(run0 + chunk, total);
+  }
   while (pos < run1) {
     while (pos >= base + (long long)a.Hkv * rq.tiles * rq.steps) {
       base += (long long)a.Hkv * rq.tiles * rq.steps;
       rq = request(a, ++r, ROWS);
     }
-    const int unit = (int)((pos - base) / rq.steps);
+    const long long into = pos - base;
+    const int unit = into < (1LL << 31) ? (int)((unsigned)into / (unsigned)rq.steps) : (int)(into / rq.steps);
     const long long unit0 = base + (long long)unit * rq.steps;
     const int h = unit / rq.tiles, tile = unit - h * rq.tiles;
     const int s_begin = (int)(pos - unit0);
@@ -581,7 +690,8 @@ __global__ void __launch_bounds__(kThreads, MINB) cache4_attn_kernel(const __gri
 
     // ---- a tile of several CTAs: the last to arrive joins the parts, in order
     if (!(starts && ends)) {
-      const int first = (int)(unit0 / chunk), final = (int)((unit0 + rq.steps - 1) / chunk);
+      const int first = parts_of ? cta - part_of : (int)(unit0 / chunk);
+      const int final = parts_of ? first + parts_of - 1 : (int)((unit0 + rq.steps - 1) / chunk);
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
@@ -637,10 +747,9 @@ cudaError_t go(Cache4AttnArgs a, cudaStream_t st) {
   // no more CTAs than the longest lengths the table allows can occupy, a run of min_chunk each
   const long long tiles = ((long long)a.max_new * (a.Hq / a.Hkv) + 8 * NT - 1) / (8 * NT);
   const long long steps = (((long long)a.max_pages << a.page_shift) + kStep - 1) / kStep;
-  const long long most = (long long)a.R * a.Hkv * tiles * steps;
-  int ctas = 148 * MINB;
-  const long long need = (most + a.min_chunk - 1) / a.min_chunk;
-  if (need < ctas) ctas = (int)need;
+  const long long parts = (long long)a.R * a.Hkv * tiles * ((steps + a.min_chunk - 1) / a.min_chunk);
+  a.roomy = parts <= 148 * MINB;
+  const int ctas = a.roomy ? (int)parts : 148 * MINB;
   kernel<<<ctas, kThreads, sizeof(S), st>>>(a);
   return cudaGetLastError();
 }

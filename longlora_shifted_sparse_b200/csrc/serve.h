@@ -73,6 +73,7 @@ struct Cache4AttnArgs {
   float* part_o;
   float* part_ml;
   int min_chunk;      // steps that a CTA takes at least
+  int roomy;          // the grid has a CTA for every min_chunk steps that the table's width allows
 };
 // few rows: bf16, d = 64, 128 or 256
 constexpr int kCache4MaxCtas = 148 * 4, kCache4PartRows = 32, kCache4PartFloats = 4096;
