@@ -39,7 +39,8 @@ bool cache_ok(int n_pages, int page_size) {
 // parts of whichever kernel runs.
 constexpr size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 constexpr size_t kAtCounters = 256;
-constexpr size_t kAtJoins = kAtCounters + round256(kCache4MaxCtas * sizeof(unsigned));
+constexpr size_t kAtJoins =
+    kAtCounters + round256((kCache4MaxCtas > kCache4SimtCtas ? kCache4MaxCtas : kCache4SimtCtas) * sizeof(unsigned));
 constexpr size_t kAtParts = kAtJoins + round256(kCache4TcCtas * 2 * sizeof(int4));
 constexpr size_t kPartsO = (size_t)2 * kCache4MaxCtas * kCache4PartFloats;
 constexpr size_t kTcPartsO = (size_t)2 * kCache4TcCtas * kCache4TcRows * 128;
@@ -47,6 +48,7 @@ constexpr size_t kPartsFloats = kPartsO + (size_t)2 * kCache4MaxCtas * 2 * kCach
 constexpr size_t kTcPartsFloats = kTcPartsO + (size_t)2 * kCache4TcCtas * 2 * kCache4TcRows;
 constexpr size_t kCache4WsBytes =
     kAtParts + sizeof(float) * (kPartsFloats > kTcPartsFloats ? kPartsFloats : kTcPartsFloats);
+static_assert((size_t)2 * kCache4SimtCtas * (256 + 2) <= kTcPartsFloats, "the splits' parts fit");
 
 // Tensor instructions: bf16 and a head dim that is a whole number of their wide loads.
 bool cache4_mma(int d, int dt) { return dt == S2_BF16 && (d == 64 || d == 128 || d == 256); }
@@ -245,12 +247,12 @@ s2_status s2attn_cache4_attn(const void* q, const void* cache, const int* block_
   a.n_pages = n_pages; a.max_pages = max_pages; a.max_new = max_new; a.scale = scale;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool bf16 = dtype == S2_BF16;
+  char* ws = static_cast<char*>(workspace);
+  a.status = reinterpret_cast<unsigned*>(ws);
+  a.counters = reinterpret_cast<unsigned*>(ws + kAtCounters);
+  a.joins = reinterpret_cast<int4*>(ws + kAtJoins);
+  a.part_o = reinterpret_cast<float*>(ws + kAtParts);
   if (cache4_mma(d, dtype)) {
-    char* ws = static_cast<char*>(workspace);
-    a.status = reinterpret_cast<unsigned*>(ws);
-    a.counters = reinterpret_cast<unsigned*>(ws + kAtCounters);
-    a.joins = reinterpret_cast<int4*>(ws + kAtJoins);
-    a.part_o = reinterpret_cast<float*>(ws + kAtParts);
     const long long rows = (long long)max_new * (H_q / H_kv);
     if (cache4_many(d, rows, (double)R * H_kv * rows * ((long long)max_pages << shift))) {
       a.part_ml = a.part_o + kTcPartsO;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from tests import serving_reference as ref
-from tests.test_serving import BF16, F32, HALF, filled, ints, normal, plan_both
+from tests.test_serving import BF16, F32, HALF, check_attention, filled, ints, normal, plan_both
 
 pytestmark = pytest.mark.gpu
 
@@ -98,6 +98,13 @@ def test_many_rows_many_requests(s2):
 
 def test_many_rows_of_a_wide_group(s2):
     check_many(s2, [50, 300], [3, 2], 300, 1, 64, 16, seed=4)           # more heads than a tile has rows
+
+
+@pytest.mark.parametrize("d,dtype", [(96, F32), (128, F32), (256, F32), (160, BF16), (32, BF16)])
+def test_long_rows_of_the_other_types(s2, d, dtype):
+    """Head dims and types that take no tensor instructions, split over their keys; no key at all among them."""
+    check_attention(s2, [5000, 0, 127, 129], [1, 0, 2, 1], 4, 2, d, 64, dtype, seed=d)
+    check_attention(s2, [20000], [1], 1, 1, d, 16, dtype, seed=d + 1)
 
 
 @pytest.mark.parametrize("scale,qscale", [(-0.1, 1.0), (0.0, 1.0), (1e-5, 3e4), (1e19, 1e-20), (0.2, 3.0)])
