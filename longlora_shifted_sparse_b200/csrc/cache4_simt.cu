@@ -1,15 +1,17 @@
 // Attention over the 4-bit cache on the CUDA cores: every type and head dim, fp32 arithmetic.
 //
-// o = softmax(q k^T * scale) v for one (token, query head) per CTA, over the keys up to the
-// token's own place. Online softmax: each of four warps takes 32 keys at a time, a key a lane
-// for the scores (a group's products with the codes are summed first, its scale and minimum
-// applied once), then a few channels a lane for the values; the warps' (maximum, sum, output)
+// o = softmax(q k^T * scale) v for one token and up to four query heads of a kv head per CTA, over
+// the keys up to the token's own place. Online softmax: each of four warps takes 32 keys at a time,
+// a key a lane for the scores (a group's products with the codes are summed first, its scale and
+// minimum applied once), then a few channels a lane for the values; the warps' (maximum, sum, output)
 // are joined at the end. Keys the mask hides are never added, whatever their slots hold.
 //
-// Bound by instructions (about ten a value). Few rows are split over the keys, so that the calls
-// that have them fill the GPU too: at least 128 keys a CTA, the parts joined by the last of a row's CTAs
-// to arrive, in order. fp32 on a B200: 100000 keys of one head of 64: 7796 us without the split, 87 with it;
-// 1000 keys, 32 heads on 32 of 128: 86 and 19; 4 requests of up to 4000, 64 on 8 of 96: 347 and 137.
+// Few rows are split over the keys, so that the calls that have them fill the GPU too: at least 128
+// keys a CTA, the parts joined by the last of a row's CTAs to arrive, in order. Codes become floats
+// through the mantissa, as conversions run at a quarter of the rate, and once for all heads of a CTA.
+// fp32 on a B200, us: one CTA a row; split; codes through the mantissa and heads together:
+// 100000 keys of one head of 64: 7796, 87, 53; 1000 keys of 32 heads on 32 of 128: 86, 19, 19;
+// 4 requests of up to 4000 keys, 64 heads on 8 of 96: 347, 137, 79. Bound by the loads' latency.
 #include <math.h>
 
 #include "cache4.cuh"
@@ -20,12 +22,21 @@ namespace s2 {
 
 constexpr int kSimtWarps = 4, kSimtSplits = 128;
 
-template <typename T>
+// Code in bits 4 i (i < 4) of `word` as code * 16^i, exactly: it is the low end of 2^23's mantissa.
+__device__ __forceinline__ float code_at(uint32_t word, int i) {
+  return __uint_as_float((word & (15u << (4 * i))) | 0x4b000000u) - 8388608.f;
+}
+
+// H query heads of one kv head a CTA.
+template <typename T, int H>
 __global__ void __launch_bounds__(kSimtWarps * 32) cache4_attn_simt_kernel(
     const __grid_constant__ Cache4AttnArgs a) {
-  __shared__ float q[256], qsum[8];
-  __shared__ float om[kSimtWarps][256], mm[kSimtWarps], ll[kSimtWarps];
-  const int t = blockIdx.x, hq = blockIdx.y, d = a.d, n = d / 32;
+  __shared__ __align__(16) float q[H][256];
+  __shared__ float qsum[H][8];
+  __shared__ float om[kSimtWarps][H][256], mm[kSimtWarps][H], ll[kSimtWarps][H];
+  __shared__ __align__(16) float ps[kSimtWarps][32][H];
+  __shared__ const uint8_t* subs[kSimtWarps][32];
+  const int t = blockIdx.x, hq = blockIdx.y * H, d = a.d, n = d / 32;
   const int h = hq / (a.Hq / a.Hkv);
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   // the request of token t: rows that no request owns stay as they are
@@ -48,21 +59,37 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache4_attn_simt_kernel(
   const int key0 = min((long long)z * per, (long long)keys), key1 = min((long long)key0 + per, (long long)keys);
   const int* table = a.table + lo * a.table_stride;
 
-  for (int x = threadIdx.x; x < d; x += blockDim.x)
-    q[x] = to_f32<T>(static_cast<const T*>(a.q)[t * a.qs[0] + hq * a.qs[1] + x]) * a.scale;
+  // The queries, and apart from them each group's sum; channel x is kept over 16^(x % 4), which code_at's factor undoes.
+  for (int i = threadIdx.x; i < H * d; i += blockDim.x) {
+    const int g = i / d, x = i - g * d;
+    q[g][x] = to_f32<T>(static_cast<const T*>(a.q)[t * a.qs[0] + (hq + g) * a.qs[1] + x]) * a.scale;
+  }
   __syncthreads();
-  if (threadIdx.x < n) {
+  if (threadIdx.x < H * n) {
+    const int g = threadIdx.x / n, j = threadIdx.x - g * n;
     float s = 0.f;
-    for (int i = 0; i < 32; i++) s += q[threadIdx.x * 32 + i];
-    qsum[threadIdx.x] = s;
+    for (int i = 0; i < 32; i++) s += q[g][j * 32 + i];
+    qsum[g][j] = s;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < H * d; i += blockDim.x) {
+    const int g = i / d, x = i - g * d;
+    q[g][x] *= __uint_as_float((127u - 4u * (x & 3)) << 23);
   }
   __syncthreads();
 
-  const int pieces = d / 4;  // half-words of four channels: lane's are lane, lane + 32
-  float m = -INFINITY, l = 0.f, acc[2][4] = {};
+  // Values: a lane has four channels (a half-word), lane and lane + 32 of them; a head of 32 or 64 leaves lanes over,
+  // which take other keys.
+  const int pieces = d / 4, at_once = pieces <= 16 ? 32 / pieces : 1;
+  const int first = at_once > 1 ? lane / pieces : 0, mine = at_once > 1 ? lane % pieces : lane;
+  float m[H], l[H], acc[H][2][4] = {};
+#pragma unroll
+  for (int g = 0; g < H; g++) m[g] = -INFINITY, l[g] = 0.f;
   for (int k0 = key0 + w * 32; k0 < key1; k0 += kSimtWarps * 32) {
     const int key = k0 + lane;
-    float s = -INFINITY;
+    float s[H];
+#pragma unroll
+    for (int g = 0; g < H; g++) s[g] = -INFINITY;
     const uint8_t* sub = nullptr;
     if (key < key1) {
       const int page = table[key >> a.page_shift];
@@ -70,149 +97,195 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache4_attn_simt_kernel(
         sub = a.cache + c4::sub_of_slot((key & ((1 << a.page_shift) - 1)), h, a.Hkv, a.page_shift, d) +
               (((size_t)page * a.Hkv) << (a.page_shift - 4)) * c4::sub_bytes(d);
         const int u = key & 15;
-        s = 0.f;
+#pragma unroll
+        for (int g = 0; g < H; g++) s[g] = 0.f;
         for (int j = 0; j < n; j++) {
-          float part = 0.f;
+          float part[H] = {};
+#pragma unroll
           for (int c = 0; c < 4; c++) {
             const uint32_t word = *reinterpret_cast<const uint32_t*>(sub + c4::k_word(u, j, c, n));
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-              part = fmaf((float)((word >> (4 * i)) & 15u), q[32 * j + 8 * c + i], part);
+            for (int half = 0; half < 2; half++) {
+              const uint32_t four = word >> (16 * half);
+              const float c0 = code_at(four, 0), c1 = code_at(four, 1), c2 = code_at(four, 2), c3 = code_at(four, 3);
+#pragma unroll
+              for (int g = 0; g < H; g++) {
+                const float4 x = *reinterpret_cast<const float4*>(&q[g][32 * j + 8 * c + 4 * half]);
+                part[g] = fmaf(c3, x.w, fmaf(c2, x.z, fmaf(c1, x.y, fmaf(c0, x.x, part[g]))));
+              }
+            }
           }
           const float sc = __half2float(*reinterpret_cast<const __half*>(sub + c4::ks_at(d) + (u * n + j) * 2));
           const float mn = __half2float(*reinterpret_cast<const __half*>(sub + c4::km_at(d) + (u * n + j) * 2));
-          s = fmaf(part, sc, fmaf(qsum[j], mn, s));
+#pragma unroll
+          for (int g = 0; g < H; g++) s[g] = fmaf(part[g], sc, fmaf(qsum[g][j], mn, s[g]));
         }
       } else {
-        s = NAN;  // a page outside the cache
+#pragma unroll
+        for (int g = 0; g < H; g++) s[g] = NAN;  // a page outside the cache
       }
     }
-    float mx = s;
+    __syncwarp();  // the last keys' weights are read
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    mx = fmaxf(m, mx);
-    const float base = mx == -INFINITY ? 0.f : mx;
-    const float p = expf(s - base), alpha = expf(m - base);
-    m = mx;
-    l = fmaf(l, alpha, p);
+    for (int g = 0; g < H; g++) {
+      float mx = s[g];
 #pragma unroll
-    for (int e = 0; e < 2; e++)
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      mx = fmaxf(m[g], mx);
+      const float base = mx == -INFINITY ? 0.f : mx;
+      const float p = expf(s[g] - base), alpha = expf(m[g] - base);
+      m[g] = mx;
+      l[g] = fmaf(l[g], alpha, p);
+      ps[w][lane][g] = p;
 #pragma unroll
-      for (int i = 0; i < 4; i++) acc[e][i] *= alpha;
+      for (int e = 0; e < 2; e++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) acc[g][e][i] *= alpha;
+    }
+    subs[w][lane] = sub;
+    __syncwarp();
     const int count = min(32, key1 - k0);
-    for (int k = 0; k < count; k++) {
-      const float pk = __shfl_sync(0xffffffffu, p, k);
-      const uint8_t* sk = reinterpret_cast<const uint8_t*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(sub), k));
+#pragma unroll 4
+    for (int k = first; k < count; k += at_once) {
+      const uint8_t* sk = subs[w][k];
       if (!sk) continue;
-      const int row = c4::v_row((k0 + k) & 15);
+      float pk[H];
+#pragma unroll
+      for (int g = 0; g < H; g++) pk[g] = ps[w][k][g];
+      const int row = c4::v_row(k & 15);
 #pragma unroll
       for (int e = 0; e < 2; e++) {
-        const int pc = lane + 32 * e;
+        const int pc = mine + 32 * e;
         if (pc < pieces) {
-          const int j = pc >> 3, g = pc & 7;
-          const uint32_t word = *reinterpret_cast<const uint16_t*>(sk + c4::vc_at(d) + c4::v_piece(row, j, g, n));
+          const int j = pc >> 3;
+          const uint32_t word = *reinterpret_cast<const uint16_t*>(sk + c4::vc_at(d) + c4::v_piece(row, j, pc & 7, n));
           const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(sk + c4::vp_at(d) + (row * n + j) * 4));
 #pragma unroll
-          for (int i = 0; i < 4; i++)
-            acc[e][i] = fmaf(pk, fmaf((float)((word >> (4 * i)) & 15u), sm.x, sm.y), acc[e][i]);
+          for (int i = 0; i < 4; i++) {
+            const float v = fmaf(code_at(word >> (4 * i), 0), sm.x, sm.y);
+#pragma unroll
+            for (int g = 0; g < H; g++) acc[g][e][i] = fmaf(pk[g], v, acc[g][e][i]);
+          }
         }
       }
     }
   }
-  l = warp_sum(l);
-  if (lane == 0) {
-    mm[w] = m;
-    ll[w] = l;
-  }
 #pragma unroll
-  for (int e = 0; e < 2; e++) {
-    const int pc = lane + 32 * e;
-    if (pc < pieces)
+  for (int g = 0; g < H; g++) {
+    const float sum = warp_sum(l[g]);
+    if (lane == 0) {
+      mm[w][g] = m[g];
+      ll[w][g] = sum;
+    }
+    for (int o = 32 / at_once; o < 32; o *= 2)
 #pragma unroll
-      for (int i = 0; i < 4; i++) om[w][32 * (pc >> 3) + 4 * (pc & 7) + i] = acc[e][i];
+      for (int i = 0; i < 4; i++) acc[g][0][i] += __shfl_xor_sync(0xffffffffu, acc[g][0][i], o);
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+      const int pc = mine + 32 * e;
+      if (pc < pieces && first == 0)
+#pragma unroll
+        for (int i = 0; i < 4; i++) om[w][g][4 * pc + i] = acc[g][e][i];
+    }
   }
   __syncthreads();
-  float M = -INFINITY, L = 0.f, f[kSimtWarps];
-  for (int i = 0; i < kSimtWarps; i++) M = fmaxf(M, mm[i]);
-  const float base = M == -INFINITY ? 0.f : M;
-  for (int i = 0; i < kSimtWarps; i++) {
-    f[i] = expf(mm[i] - base);
-    L = fmaf(ll[i], f[i], L);
-  }
-  if (splits > 1) {
-    const size_t row = (size_t)t * a.Hq + hq, rows = (size_t)a.T * a.Hq;
-    float* part = a.part_o + (row * gridDim.z + z) * d;
-    float* ml = a.part_o + rows * gridDim.z * d + row * gridDim.z * 2;
+  const size_t row = (size_t)t * a.Hq + hq;  // the first head's row
+  const size_t parts = (size_t)a.T * a.Hq * gridDim.z;
+  float* part_ml = a.part_o + parts * d;
+  for (int g = 0; g < H; g++) {
+    float M = -INFINITY, L = 0.f, f[kSimtWarps];
+    for (int i = 0; i < kSimtWarps; i++) M = fmaxf(M, mm[i][g]);
+    const float base = M == -INFINITY ? 0.f : M;
+    for (int i = 0; i < kSimtWarps; i++) {
+      f[i] = expf(mm[i][g] - base);
+      L = fmaf(ll[i][g], f[i], L);
+    }
+    // a row that sees no key has L = 0: its output is 0 and its log-sum-exp -inf
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const size_t part = (row + g) * gridDim.z + z;
     for (int x = threadIdx.x; x < d; x += blockDim.x) {
       float o = 0.f;
-      for (int i = 0; i < kSimtWarps; i++) o = fmaf(om[i][x], f[i], o);
-      part[x] = o;
+      for (int i = 0; i < kSimtWarps; i++) o = fmaf(om[i][g][x], f[i], o);
+      if (splits > 1)
+        a.part_o[part * d + x] = o;
+      else
+        static_cast<T*>(a.o)[(row + g) * d + x] = from_f32<T>(o * inv);
     }
     if (threadIdx.x == 0) {
-      ml[2 * z] = M;
-      ml[2 * z + 1] = L;
+      if (splits > 1) {
+        part_ml[2 * part] = M;
+        part_ml[2 * part + 1] = L;
+      } else if (a.lse) {
+        a.lse[(size_t)(hq + g) * a.T + t] = L == 0.f ? -INFINITY : base + logf(L);
+      }
     }
-    __threadfence();
+  }
+  if (splits == 1) return;
+
+  __threadfence();
+  __syncthreads();
+  __shared__ int joins;
+  if (threadIdx.x == 0) {
+    joins = (int)atomicAdd(a.counters + row / H, 1u) == splits - 1;
+    if (joins) a.counters[row / H] = 0u;  // ready for the next call
+  }
+  __syncthreads();
+  if (!joins) return;
+  __threadfence();
+  // a part a thread: its weight; then the sums over the parts, in order
+  static_assert(kSimtSplits <= kSimtWarps * 32, "a thread a part");
+  __shared__ float weight[kSimtSplits], sum[kSimtSplits];
+  const int p = threadIdx.x;
+  for (int g = 0; g < H; g++) {
+    const float* ml = part_ml + (row + g) * gridDim.z * 2;
     __syncthreads();
-    __shared__ int joins;
-    if (threadIdx.x == 0) {
-      joins = (int)atomicAdd(a.counters + row, 1u) == splits - 1;
-      if (joins) a.counters[row] = 0u;  // ready for the next call
-    }
+    if (p < splits) weight[p] = __ldcg(ml + 2 * p);
     __syncthreads();
-    if (!joins) return;
-    __threadfence();
-    // a part a thread: its weight; then the sums over the parts, in order
-    static_assert(kSimtSplits <= kSimtWarps * 32, "a thread a part");
-    __shared__ float weight[kSimtSplits], sum[kSimtSplits];
-    const int mine = threadIdx.x;
-    if (mine < splits) weight[mine] = __ldcg(ml + 2 * mine);
-    __syncthreads();
-    M = -INFINITY;
+    float M = -INFINITY, L = 0.f;
     for (int i = 0; i < splits; i++) M = fmaxf(M, weight[i]);
     const float top = M == -INFINITY ? 0.f : M;
     __syncthreads();
-    if (mine < splits) {
-      weight[mine] = expf(weight[mine] - top);
-      sum[mine] = __ldcg(ml + 2 * mine + 1);
+    if (p < splits) {
+      weight[p] = expf(weight[p] - top);
+      sum[p] = __ldcg(ml + 2 * p + 1);
     }
     __syncthreads();
-    L = 0.f;
     for (int i = 0; i < splits; i++) L = fmaf(sum[i], weight[i], L);
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    const float* parts = a.part_o + row * gridDim.z * d;
+    const float* from = a.part_o + (row + g) * gridDim.z * d;
     for (int x = threadIdx.x; x < d; x += blockDim.x) {
       float o = 0.f;
 #pragma unroll 8
-      for (int i = 0; i < splits; i++) o = fmaf(__ldcg(parts + (size_t)i * d + x), weight[i], o);
-      static_cast<T*>(a.o)[row * d + x] = from_f32<T>(o * inv);
+      for (int i = 0; i < splits; i++) o = fmaf(__ldcg(from + (size_t)i * d + x), weight[i], o);
+      static_cast<T*>(a.o)[(row + g) * d + x] = from_f32<T>(o * inv);
     }
-    if (a.lse && threadIdx.x == 0) a.lse[(size_t)hq * a.T + t] = L == 0.f ? -INFINITY : top + logf(L);
-    return;
+    if (a.lse && threadIdx.x == 0) a.lse[(size_t)(hq + g) * a.T + t] = L == 0.f ? -INFINITY : top + logf(L);
   }
-  // a row that sees no key has L = 0: its output is 0 and its log-sum-exp -inf
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  for (int x = threadIdx.x; x < d; x += blockDim.x) {
-    float o = 0.f;
-    for (int i = 0; i < kSimtWarps; i++) o = fmaf(om[i][x], f[i], o);
-    static_cast<T*>(a.o)[((size_t)t * a.Hq + hq) * d + x] = from_f32<T>(o * inv);
-  }
-  if (a.lse && threadIdx.x == 0) a.lse[(size_t)hq * a.T + t] = L == 0.f ? -INFINITY : base + logf(L);
 }
 
-cudaError_t launch_cache4_attn_simt(const Cache4AttnArgs& a, bool bf16, cudaStream_t st) {
+template <int H>
+cudaError_t run_simt(const Cache4AttnArgs& a, bool bf16, long long most, cudaStream_t st) {
   // few rows: so many splits that about eight CTAs an SM have keys, if the table's width allows
-  const long long rows = (long long)a.T * a.Hq, most = (((long long)a.max_pages << a.page_shift) + 127) / 128;
+  const long long rows = (long long)a.T * (a.Hq / H);
   long long splits = rows >= kCache4SimtCtas ? 1 : (kCache4SimtCtas + rows - 1) / rows;
   if (splits > most) splits = most;
   if (splits > kSimtSplits) splits = kSimtSplits;
-  const dim3 grid(a.T, a.Hq, (unsigned)splits);
+  const dim3 grid(a.T, a.Hq / H, (unsigned)splits);
   if (bf16)
-    cache4_attn_simt_kernel<__nv_bfloat16><<<grid, kSimtWarps * 32, 0, st>>>(a);
+    cache4_attn_simt_kernel<__nv_bfloat16, H><<<grid, kSimtWarps * 32, 0, st>>>(a);
   else
-    cache4_attn_simt_kernel<float><<<grid, kSimtWarps * 32, 0, st>>>(a);
+    cache4_attn_simt_kernel<float, H><<<grid, kSimtWarps * 32, 0, st>>>(a);
   return cudaGetLastError();
+}
+
+cudaError_t launch_cache4_attn_simt(const Cache4AttnArgs& a, bool bf16, cudaStream_t st) {
+  const long long most = (((long long)a.max_pages << a.page_shift) + 127) / 128;
+  // Heads share a CTA, and with it the decoding of the codes, where that leaves two CTAs with keys an SM.
+  const int group = a.Hq / a.Hkv;
+  const long long blocks = (long long)a.T * a.Hq * (most < kSimtSplits ? most : kSimtSplits);
+  if (group % 4 == 0 && blocks / 4 >= 2 * 148) return run_simt<4>(a, bf16, most, st);
+  if (group % 2 == 0 && blocks / 2 >= 2 * 148) return run_simt<2>(a, bf16, most, st);
+  return run_simt<1>(a, bf16, most, st);
 }
 
 }  // namespace s2

@@ -81,7 +81,7 @@ cudaError_t launch_cache4_attn(Cache4AttnArgs a, cudaStream_t st);
 // many rows: bf16, d = 64 or 128
 constexpr int kCache4TcCtas = 148, kCache4TcRows = 256;
 cudaError_t launch_cache4_tc(Cache4AttnArgs a, cudaStream_t st);
-// any type and head dim; splits of up to 2 kCache4SimtCtas parts of d + 2 floats in part_o
+// any type and head dim; splits of up to 2 kCache4SimtCtas parts of four heads of d + 2 floats in part_o
 constexpr int kCache4SimtCtas = 148 * 8;
 cudaError_t launch_cache4_attn_simt(const Cache4AttnArgs& a, bool bf16, cudaStream_t st);
 

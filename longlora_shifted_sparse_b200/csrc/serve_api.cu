@@ -48,7 +48,7 @@ constexpr size_t kPartsFloats = kPartsO + (size_t)2 * kCache4MaxCtas * 2 * kCach
 constexpr size_t kTcPartsFloats = kTcPartsO + (size_t)2 * kCache4TcCtas * 2 * kCache4TcRows;
 constexpr size_t kCache4WsBytes =
     kAtParts + sizeof(float) * (kPartsFloats > kTcPartsFloats ? kPartsFloats : kTcPartsFloats);
-static_assert((size_t)2 * kCache4SimtCtas * (256 + 2) <= kTcPartsFloats, "the splits' parts fit");
+static_assert((size_t)2 * kCache4SimtCtas * 4 * (256 + 2) <= kTcPartsFloats, "the splits' parts fit");
 
 // Tensor instructions: bf16 and a head dim that is a whole number of their wide loads.
 bool cache4_mma(int d, int dt) { return dt == S2_BF16 && (d == 64 || d == 128 || d == 256); }
