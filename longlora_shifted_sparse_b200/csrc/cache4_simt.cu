@@ -9,9 +9,11 @@
 // Few rows are split over the keys, so that the calls that have them fill the GPU too: at least 128
 // keys a CTA, the parts joined by the last of a row's CTAs to arrive, in order. Codes become floats
 // through the mantissa, as conversions run at a quarter of the rate, and once for all heads of a CTA.
-// fp32 on a B200, us: one CTA a row; split; codes through the mantissa and heads together:
-// 100000 keys of one head of 64: 7796, 87, 53; 1000 keys of 32 heads on 32 of 128: 86, 19, 19;
-// 4 requests of up to 4000 keys, 64 heads on 8 of 96: 347, 137, 79. Bound by the loads' latency.
+// Each warp copies its 32 keys, two sub-blocks, to shared memory before it reads them: its loads of codes
+// are of four bytes, half a row and more apart.
+// fp32 on a B200, us: one CTA a row; split; codes through the mantissa and heads together; keys copied:
+// 100000 keys of one head of 64: 7796, 87, 53, 39; 1000 keys of 32 heads on 32 of 128: 86, 19, 19, 16;
+// 4 requests of up to 4000 keys, 64 heads on 8 of 96: 347, 137, 79, 66.
 #include <math.h>
 
 #include "cache4.cuh"
@@ -27,15 +29,23 @@ __device__ __forceinline__ float code_at(uint32_t word, int i) {
   return __uint_as_float((word & (15u << (4 * i))) | 0x4b000000u) - 8388608.f;
 }
 
+// A staged sub-block: its rows of k codes lie an odd number of 16-byte pieces apart, so that a warp's
+// loads of one word of its rows meet four at a bank, the least that 16-byte copies allow.
+__host__ __device__ constexpr int staged_bytes(int d) { return c4::sub_bytes(d) + 256; }
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // H query heads of one kv head a CTA.
 template <typename T, int H>
 __global__ void __launch_bounds__(kSimtWarps * 32) cache4_attn_simt_kernel(
     const __grid_constant__ Cache4AttnArgs a) {
   __shared__ __align__(16) float q[H][256];
   __shared__ float qsum[H][8];
-  __shared__ float om[kSimtWarps][H][256], mm[kSimtWarps][H], ll[kSimtWarps][H];
+  __shared__ float mm[kSimtWarps][H], ll[kSimtWarps][H];
   __shared__ __align__(16) float ps[kSimtWarps][32][H];
-  __shared__ const uint8_t* subs[kSimtWarps][32];
+  extern __shared__ __align__(16) uint8_t staged[];  // [warp][2 sub-blocks]; at the end the warps' outputs
   const int t = blockIdx.x, hq = blockIdx.y * H, d = a.d, n = d / 32;
   const int h = hq / (a.Hq / a.Hkv);
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -85,25 +95,50 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache4_attn_simt_kernel(
   float m[H], l[H], acc[H][2][4] = {};
 #pragma unroll
   for (int g = 0; g < H; g++) m[g] = -INFINITY, l[g] = 0.f;
+  // Copies a step's keys, two sub-blocks; a bit for each that lies on a page of the cache. A second step's place would
+  // take the room of the CTAs that hide the copies' latency: 8 heads of 128, 100000 keys 121 us so and 127 with it,
+  // 4 heads of 256, 50000 keys 74 and 99; nothing gained by more than 5%.
+  const int size = staged_bytes(d), k_row = 16 * (n | 1), rest = 16 * (k_row - 16 * n), inverse = 65536 / n + 1;
+  uint8_t* const own = staged + w * 2 * size;
+  auto fetch = [&](int k0) {
+    unsigned ok = 0;
+    for (int i = 0; i < 2; i++) {
+      const int key = k0 + 16 * i;
+      const int page = key < key1 ? table[key >> a.page_shift] : -1;
+      if (page < 0 || page >= a.n_pages) continue;
+      ok |= 1u << i;
+      const uint8_t* sub = a.cache +
+                           c4::sub_of_slot((key & ((1 << a.page_shift) - 1)), h, a.Hkv, a.page_shift, d) +
+                           (((size_t)page * a.Hkv) << (a.page_shift - 4)) * c4::sub_bytes(d);
+      const uint32_t to = (uint32_t)__cvta_generic_to_shared(own + i * size);
+      for (int p = lane; p < 40 * n; p += 32) {
+        const int r = (p * inverse) >> 16;  // p / n, as p < 128 where it is used
+        copy16(to + (p < 16 * n ? r * k_row + (p - r * n) * 16 : 16 * p + rest), sub + 16 * p);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    return ok;
+  };
   for (int k0 = key0 + w * 32; k0 < key1; k0 += kSimtWarps * 32) {
+    const unsigned ok = fetch(k0);
     const int key = k0 + lane;
     float s[H];
 #pragma unroll
     for (int g = 0; g < H; g++) s[g] = -INFINITY;
-    const uint8_t* sub = nullptr;
     if (key < key1) {
-      const int page = table[key >> a.page_shift];
-      if (page >= 0 && page < a.n_pages) {
-        sub = a.cache + c4::sub_of_slot((key & ((1 << a.page_shift) - 1)), h, a.Hkv, a.page_shift, d) +
-              (((size_t)page * a.Hkv) << (a.page_shift - 4)) * c4::sub_bytes(d);
-        const int u = key & 15;
+      if (ok >> (lane >> 4) & 1) {
+        const uint8_t* sub = own + (lane >> 4) * size;
+        const int u = lane & 15;
+        const uint8_t* codes = sub + u * (k_row - 16 * n);
+        sub += rest;
 #pragma unroll
         for (int g = 0; g < H; g++) s[g] = 0.f;
         for (int j = 0; j < n; j++) {
           float part[H] = {};
 #pragma unroll
           for (int c = 0; c < 4; c++) {
-            const uint32_t word = *reinterpret_cast<const uint32_t*>(sub + c4::k_word(u, j, c, n));
+            const uint32_t word = *reinterpret_cast<const uint32_t*>(codes + c4::k_word(u, j, c, n));
 #pragma unroll
             for (int half = 0; half < 2; half++) {
               const uint32_t four = word >> (16 * half);
@@ -125,7 +160,6 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache4_attn_simt_kernel(
         for (int g = 0; g < H; g++) s[g] = NAN;  // a page outside the cache
       }
     }
-    __syncwarp();  // the last keys' weights are read
 #pragma unroll
     for (int g = 0; g < H; g++) {
       float mx = s[g];
@@ -142,13 +176,12 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache4_attn_simt_kernel(
 #pragma unroll
         for (int i = 0; i < 4; i++) acc[g][e][i] *= alpha;
     }
-    subs[w][lane] = sub;
     __syncwarp();
     const int count = min(32, key1 - k0);
 #pragma unroll 4
     for (int k = first; k < count; k += at_once) {
-      const uint8_t* sk = subs[w][k];
-      if (!sk) continue;
+      if (!(ok >> (k >> 4) & 1)) continue;
+      const uint8_t* sk = own + (k >> 4) * size + rest;
       float pk[H];
 #pragma unroll
       for (int g = 0; g < H; g++) pk[g] = ps[w][k][g];
@@ -169,7 +202,10 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache4_attn_simt_kernel(
         }
       }
     }
+    __syncwarp();  // this step's keys and weights are read
   }
+  __syncthreads();
+  float* const om = reinterpret_cast<float*>(staged);  // [warp][H][d]
 #pragma unroll
   for (int g = 0; g < H; g++) {
     const float sum = warp_sum(l[g]);
@@ -185,7 +221,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache4_attn_simt_kernel(
       const int pc = mine + 32 * e;
       if (pc < pieces && first == 0)
 #pragma unroll
-        for (int i = 0; i < 4; i++) om[w][g][4 * pc + i] = acc[g][e][i];
+        for (int i = 0; i < 4; i++) om[(w * H + g) * d + 4 * pc + i] = acc[g][e][i];
     }
   }
   __syncthreads();
@@ -205,7 +241,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache4_attn_simt_kernel(
     const size_t part = (row + g) * gridDim.z + z;
     for (int x = threadIdx.x; x < d; x += blockDim.x) {
       float o = 0.f;
-      for (int i = 0; i < kSimtWarps; i++) o = fmaf(om[i][g][x], f[i], o);
+      for (int i = 0; i < kSimtWarps; i++) o = fmaf(om[(i * H + g) * d + x], f[i], o);
       if (splits > 1)
         a.part_o[part * d + x] = o;
       else
@@ -271,10 +307,12 @@ cudaError_t run_simt(const Cache4AttnArgs& a, bool bf16, long long most, cudaStr
   if (splits > most) splits = most;
   if (splits > kSimtSplits) splits = kSimtSplits;
   const dim3 grid(a.T, a.Hq / H, (unsigned)splits);
-  if (bf16)
-    cache4_attn_simt_kernel<__nv_bfloat16, H><<<grid, kSimtWarps * 32, 0, st>>>(a);
-  else
-    cache4_attn_simt_kernel<float, H><<<grid, kSimtWarps * 32, 0, st>>>(a);
+  auto kernel = bf16 ? cache4_attn_simt_kernel<__nv_bfloat16, H> : cache4_attn_simt_kernel<float, H>;
+  const int bytes = kSimtWarps * 2 * staged_bytes(a.d);
+  // set on every call: it is per device, and costs no synchronisation
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kSimtWarps * 32, bytes, st>>>(a);
   return cudaGetLastError();
 }
 
