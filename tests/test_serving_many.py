@@ -300,3 +300,53 @@ def test_a_wait_that_gave_up_is_reported(s2):
     assert s2.device_status(ws) == s2.S2_ERR_DEVICE_TIMEOUT
     assert torch.equal(s2.cache4_attention(*args, ws=ws), want)
     assert s2.device_status(ws) == s2.S2_OK
+
+
+@pytest.mark.parametrize("Hq,H", [(6, 2), (8, 2), (10, 5), (3, 1)])
+@pytest.mark.parametrize("d", [32, 64, 192])
+def test_shared_heads_of_the_other_types(s2, Hq, H, d):
+    """Groups of one to four heads a block, one or many splits, requests without tokens between."""
+    check_attention(s2, [700, 3, 40, 2000, 129], [40, 0, 5, 60, 2], Hq, H, d, 16, F32, seed=Hq + d)
+    check_attention(s2, [12000, 900], [1, 1], Hq, H, d, 128, F32, seed=Hq * d)
+
+
+@pytest.mark.parametrize("bad", [-1, 10 ** 6])
+def test_pages_outside_the_cache_of_the_other_types(s2, bad):
+    """A page that is none makes its request's rows NaN and no other's; one that lies behind every seen key is not read."""
+    lens, new, Hq, H, d, P = [3000, 500, 2000], [1, 1, 1], 4, 1, 96, 64
+    cache, table, _ = filled(s2, lens, P, H, d, 5)
+    q = normal(6, 3, Hq, d, dtype=F32)
+    args = (ints(lens), ints([0, 1, 2, 3]), 1)
+    ws = s2.cache4_workspace()
+    o = s2.cache4_attention(q, cache, table, *args, ws=ws)
+    wrong = table.clone()
+    wrong[0, 20] = bad
+    wrong[1, 8:] = bad
+    got = s2.cache4_attention(q, cache, wrong, *args, ws=ws)
+    assert got[0].isnan().all() and torch.equal(got[1:], o[1:])
+    assert torch.equal(s2.cache4_attention(q, cache, table, *args, ws=ws), o)      # nothing of it stays in the workspace
+
+
+def test_captured_calls_of_the_other_types(s2):
+    """Replays follow the lengths on the GPU, also to none, and share a workspace with calls between."""
+    lens, P, Hq, H, d = [6000, 2500], 64, 8, 2, 64
+    cache, table, _ = filled(s2, lens, P, H, d, 8)
+    q = normal(9, 2, Hq, d, dtype=F32)
+    n, cu, ws = ints(lens), ints([0, 1, 2]), s2.cache4_workspace()
+    out = torch.empty_like(q)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream):
+        s2.cache4_attention(q, cache, table, n, cu, 1, ws=ws, out=out)
+        stream.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            s2.cache4_attention(q, cache, table, n, cu, 1, ws=ws, out=out)
+        for now in ([6000, 2500], [1, 0], [129, 2400], [5999, 128]):
+            n.copy_(ints(now))
+            graph.replay()
+            want = s2.cache4_attention(q, cache, table, n, cu, 1, ws=ws)
+            assert torch.equal(out, want)
+            if 0 in now:
+                assert (out[now.index(0)] == 0).all()
+    torch.cuda.current_stream().wait_stream(stream)
