@@ -12,7 +12,10 @@
 // and shared by all heads: fp64 work per token is rot/2 products. A thread keeps the (cos, sin) of its
 // channels over the heads and has one row in flight; eight CTAs an SM then hide the latency better
 // than more rows a thread (32768 tokens, 64 heads of 128 in bf16: 177 us, 6.1 TB/s, against 182 with
-// two rows and 215 with four).
+// two rows and 215 with four). Halves keep two runs and a (cos, sin) for each of their pairs: of bf16, four
+// pairs of 8 bytes and five CTAs an SM (the same tokens 235 us; eight pairs of 16 bytes 299, two pairs 277, six
+// CTAs 313, which spills). Threads that few heads leave over take other tokens: 2 x 30000 tokens, 4 heads of 80 in
+// halves 238 us without that, 49; 57835 tokens of 4 heads of 128 90 us and 41.
 #include "common.cuh"
 #include "serve.h"
 #include "sm100.cuh"
@@ -21,13 +24,19 @@ namespace s2 {
 
 constexpr int kRopeThreads = 256;
 
-// A CTA takes `tokens` consecutive tokens. Threads x: the units of a head row; threads y: heads.
+// A CTA takes `tokens` consecutive tokens. Threads x: the units of a head row; threads y: `rows` heads of
+// one token or, when that is not all of them, of several.
 // A unit is V channels (interleaved), V pairs (half), or V channels beyond `rot`; V = 16 bytes
-// where strides and widths allow it, else one pair.
+// (8 for bf16 halves) where strides and widths allow it, else one pair.
 template <typename T, int V>
 __device__ __forceinline__ void load_v(const T* p, float (&x)[V]) {
   if constexpr (V * sizeof(T) == 16) {
     const uint4 raw = __ldcs(reinterpret_cast<const uint4*>(p));
+    const T* y = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+    for (int i = 0; i < V; i++) x[i] = to_f32<T>(y[i]);
+  } else if constexpr (V * sizeof(T) == 8) {
+    const uint2 raw = __ldcs(reinterpret_cast<const uint2*>(p));
     const T* y = reinterpret_cast<const T*>(&raw);
 #pragma unroll
     for (int i = 0; i < V; i++) x[i] = to_f32<T>(y[i]);
@@ -44,6 +53,12 @@ __device__ __forceinline__ void store_v(T* p, const float (&x)[V]) {
 #pragma unroll
     for (int i = 0; i < V; i++) y[i] = from_f32<T>(x[i]);
     __stcs(reinterpret_cast<uint4*>(p), raw);
+  } else if constexpr (V * sizeof(T) == 8) {
+    uint2 raw;
+    T* y = reinterpret_cast<T*>(&raw);
+#pragma unroll
+    for (int i = 0; i < V; i++) y[i] = from_f32<T>(x[i]);
+    __stcs(reinterpret_cast<uint2*>(p), raw);
   } else {
 #pragma unroll
     for (int i = 0; i < V; i++) p[i] = from_f32<T>(x[i]);
@@ -77,7 +92,8 @@ __device__ __forceinline__ void rotate_heads(const T* src, T* dst, long long is,
 }
 
 template <typename T, int V, bool kHalf>
-__global__ void __launch_bounds__(kRopeThreads, !kHalf ? 8 : V <= 4 ? 6 : 3) rope_kernel(const __grid_constant__ RopeArgs a, int tokens) {
+__global__ void __launch_bounds__(kRopeThreads, !kHalf ? 8 : V == 4 && sizeof(T) == 2 ? 5 : 6)
+    rope_kernel(const __grid_constant__ RopeArgs a, int tokens, int rows) {
   extern __shared__ float2 cs[];  // [tokens][rot / 2]
   constexpr int kPairs = kHalf ? V : V / 2;
   const int pairs = a.rot / 2;
@@ -106,22 +122,23 @@ __global__ void __launch_bounds__(kRopeThreads, !kHalf ? 8 : V <= 4 ? 6 : 3) rop
   for (int u = threadIdx.x; u < units; u += blockDim.x) {
     const bool rotated = u < rot_units;
     const int at = rotated ? u * (kHalf ? kPairs : V) : a.rot + (u - rot_units) * V;
-    int b = b0, n = n0;
-    for (int t = 0; t < nt; t++) {
+    const int first = threadIdx.y % rows, apart = blockDim.y / rows;  // the thread's first head; its tokens' distance
+    for (int t = threadIdx.y / rows; t < nt; t += apart) {
+      int b = b0, n = n0 + t;
+      while (n >= a.N) {
+        n -= a.N;
+        b++;
+      }
       float2 mine[kPairs];
 #pragma unroll
       for (int e = 0; e < kPairs; e++) mine[e] = rotated ? cs[t * pairs + u * kPairs + e] : make_float2(1.f, 0.f);
       rotate_heads<T, V, kHalf, kPairs>(static_cast<const T*>(a.q) + b * a.qs[0] + n * a.qs[1],
                                                static_cast<T*>(a.qo) + b * a.qos[0] + n * a.qos[1], a.qs[2], a.qos[2],
-                                               a.Hq, threadIdx.y, blockDim.y, pairs, at, rotated, mine);
+                                               a.Hq, first, rows, pairs, at, rotated, mine);
       if (a.k)
         rotate_heads<T, V, kHalf, kPairs>(static_cast<const T*>(a.k) + b * a.ks[0] + n * a.ks[1],
                                                  static_cast<T*>(a.ko) + b * a.kos[0] + n * a.kos[1], a.ks[2], a.kos[2],
-                                                 a.Hkv, threadIdx.y, blockDim.y, pairs, at, rotated, mine);
-      if (++n == a.N) {
-        n = 0;
-        b++;
-      }
+                                                 a.Hkv, first, rows, pairs, at, rotated, mine);
     }
   }
 }
@@ -130,22 +147,27 @@ template <typename T, int V, bool kHalf>
 static cudaError_t go(const RopeArgs& a, cudaStream_t st) {
   const long long tokens = (long long)a.B * a.N;
   const int units = (kHalf ? a.rot / 2 / V : a.rot / V) + (a.d - a.rot) / V;
-  const int tile = tokens >= 4 * 592 ? 4 : 1;
-  const dim3 block(units < 32 ? units : 32, kRopeThreads / (units < 32 ? units : 32));
+  const int wide = units < 32 ? units : 32, most = kRopeThreads / wide;
+  const int heads = a.k && a.Hkv > a.Hq ? a.Hkv : a.Hq, rows = heads < most ? heads : most, apart = most / rows;
+  // few heads: the threads that are left take other tokens
+  long long tile = tokens < 4 * 592 ? 1 : apart < 4 ? 4 : apart < tokens / 592 ? apart : tokens / 592;
+  while (tile > 4 && tile * a.rot / 2 * sizeof(float2) > 16384) tile /= 2;
+  const dim3 block(wide, rows * apart);
   rope_kernel<T, V, kHalf><<<dim3((unsigned)((tokens + tile - 1) / tile)), block, tile * a.rot / 2 * sizeof(float2), st>>>(
-      a, tile);
+      a, (int)tile, rows);
   return cudaGetLastError();
 }
 
 template <typename T>
 static cudaError_t go_type(const RopeArgs& a, cudaStream_t st) {
-  constexpr int V = 16 / sizeof(T);
-  // 16-byte units need every row and every run of channels to start and end on 16 bytes
+  constexpr int V = 16 / sizeof(T), H = V < 4 ? V : 4;
+  // wide units need every row and every run of channels to start and end on one
   // (the pointers do); a unit of the half layout is V pairs, so its halves must too
-  bool wide = a.d % V == 0 && a.rot % (a.half ? 2 * V : V) == 0;
-  for (int i = 0; i < 3; i++) wide = wide && a.qs[i] % V == 0 && (!a.k || a.ks[i] % V == 0);
+  const int unit = a.half ? H : V;
+  bool wide = a.d % unit == 0 && a.rot % (a.half ? 2 * H : V) == 0;
+  for (int i = 0; i < 3; i++) wide = wide && a.qs[i] % unit == 0 && (!a.k || a.ks[i] % unit == 0);
   if (a.half)
-    return wide ? go<T, V, true>(a, st) : go<T, 1, true>(a, st);
+    return wide ? go<T, H, true>(a, st) : go<T, 1, true>(a, st);
   return wide ? go<T, V, false>(a, st) : go<T, 2, false>(a, st);
 }
 

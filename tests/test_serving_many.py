@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from tests import serving_reference as ref
-from tests.test_serving import BF16, F32, HALF, check_attention, filled, ints, normal, plan_both
+from tests.test_serving import BF16, F32, HALF, check_attention, filled, ints, normal, plan_both, rope_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -350,3 +350,22 @@ def test_captured_calls_of_the_other_types(s2):
             if 0 in now:
                 assert (out[now.index(0)] == 0).all()
     torch.cuda.current_stream().wait_stream(stream)
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,N,Hq,Hkv,d,rot", [(5, 1001, 2, 2, 128, 128), (900, 3, 1, 1, 64, 64), (3, 2000, 3, 1, 80, 80),
+                                              (2, 3001, 5, 2, 256, 256), (4, 700, 3, 2, 44, 24), (1, 9001, 1, 1, 8, 8)])
+def test_rope_few_heads(s2, layout, dtype, B, N, Hq, Hkv, d, rot):
+    """Threads share out tokens as well as heads, over the ends of a batch's rows; rows that start on 8 bytes only."""
+    q, k = normal(1, B, N, Hq, d, dtype=dtype), normal(2, B, N, Hkv, d, dtype=dtype)
+    pos = torch.randint(0, 1 << 20, (B, N), generator=torch.Generator().manual_seed(5)).cuda()
+    theta, table = ref.freqs(rot, 10000.0, 8.0, 4096), s2.rope_freqs(rot, 10000.0, 8.0, 4096)
+    q2, k2 = s2.rope(q, k, pos, table, layout=layout, mscale=1.25)
+    for got, x in ((q2, q), (k2, k)):
+        want = ref.rope(x, pos, theta, layout, 1.25, False)
+        assert ((got.double() - want).abs() <= rope_bound(x, want, rot, layout, 1.25)).all()
+    alone = s2.rope(k, None, pos, table, layout=layout, mscale=1.25)[0]
+    assert torch.equal(alone, k2)
+    q3, k3 = s2.rope(q, k, pos, table, layout=layout, mscale=1.25, in_place=True)
+    assert torch.equal(q3, q2) and torch.equal(k3, k2) and q3.data_ptr() == q.data_ptr()
