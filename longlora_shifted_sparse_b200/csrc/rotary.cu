@@ -27,15 +27,16 @@ constexpr int kRopeThreads = 256;
 // A CTA takes `tokens` consecutive tokens. Threads x: the units of a head row; threads y: `rows` heads of
 // one token or, when that is not all of them, of several.
 // A unit is V channels (interleaved), V pairs (half), or V channels beyond `rot`; V = 16 bytes
-// (8 for bf16 halves) where strides and widths allow it, else one pair.
-template <typename T, int V>
+// (8 for bf16 halves) where strides and widths allow it, else one pair. kVector: every unit starts on a
+// multiple of its own 8 or 16 bytes; else its elements are taken one by one.
+template <typename T, int V, bool kVector>
 __device__ __forceinline__ void load_v(const T* p, float (&x)[V]) {
-  if constexpr (V * sizeof(T) == 16) {
+  if constexpr (kVector && V * sizeof(T) == 16) {
     const uint4 raw = __ldcs(reinterpret_cast<const uint4*>(p));
     const T* y = reinterpret_cast<const T*>(&raw);
 #pragma unroll
     for (int i = 0; i < V; i++) x[i] = to_f32<T>(y[i]);
-  } else if constexpr (V * sizeof(T) == 8) {
+  } else if constexpr (kVector && V * sizeof(T) == 8) {
     const uint2 raw = __ldcs(reinterpret_cast<const uint2*>(p));
     const T* y = reinterpret_cast<const T*>(&raw);
 #pragma unroll
@@ -45,15 +46,15 @@ __device__ __forceinline__ void load_v(const T* p, float (&x)[V]) {
     for (int i = 0; i < V; i++) x[i] = to_f32<T>(p[i]);
   }
 }
-template <typename T, int V>
+template <typename T, int V, bool kVector>
 __device__ __forceinline__ void store_v(T* p, const float (&x)[V]) {
-  if constexpr (V * sizeof(T) == 16) {
+  if constexpr (kVector && V * sizeof(T) == 16) {
     uint4 raw;
     T* y = reinterpret_cast<T*>(&raw);
 #pragma unroll
     for (int i = 0; i < V; i++) y[i] = from_f32<T>(x[i]);
     __stcs(reinterpret_cast<uint4*>(p), raw);
-  } else if constexpr (V * sizeof(T) == 8) {
+  } else if constexpr (kVector && V * sizeof(T) == 8) {
     uint2 raw;
     T* y = reinterpret_cast<T*>(&raw);
 #pragma unroll
@@ -66,7 +67,7 @@ __device__ __forceinline__ void store_v(T* p, const float (&x)[V]) {
 }
 
 // One of q and k: the heads of a token that this thread takes, with its (cos, sin) in registers.
-template <typename T, int V, bool kHalf, int kPairs>
+template <typename T, int V, bool kHalf, bool kVector, int kPairs>
 __device__ __forceinline__ void rotate_heads(const T* src, T* dst, long long is, long long os, int heads, int first,
                                              int step, int pairs, int at, bool rotated, const float2 (&cs)[kPairs]) {
   using namespace sm100;
@@ -75,8 +76,8 @@ __device__ __forceinline__ void rotate_heads(const T* src, T* dst, long long is,
   dst += at;
   for (int h = first; h < heads; h += step) {
     float x[X][V];
-    load_v<T, V>(src + h * is, x[0]);
-    if (kHalf && rotated) load_v<T, V>(src + h * is + pairs, x[X - 1]);
+    load_v<T, V, kVector>(src + h * is, x[0]);
+    if (kHalf && rotated) load_v<T, V, kVector>(src + h * is + pairs, x[X - 1]);
     if (rotated) {
 #pragma unroll
       for (int e = 0; e < kPairs; e++) {
@@ -86,12 +87,12 @@ __device__ __forceinline__ void rotate_heads(const T* src, T* dst, long long is,
         f2unpack(y, a, b);
       }
     }
-    store_v<T, V>(dst + h * os, x[0]);
-    if (kHalf && rotated) store_v<T, V>(dst + h * os + pairs, x[X - 1]);
+    store_v<T, V, kVector>(dst + h * os, x[0]);
+    if (kHalf && rotated) store_v<T, V, kVector>(dst + h * os + pairs, x[X - 1]);
   }
 }
 
-template <typename T, int V, bool kHalf>
+template <typename T, int V, bool kHalf, bool kVector>
 __global__ void __launch_bounds__(kRopeThreads, !kHalf ? 8 : V == 4 && sizeof(T) == 2 ? 5 : 6)
     rope_kernel(const __grid_constant__ RopeArgs a, int tokens, int rows) {
   extern __shared__ float2 cs[];  // [tokens][rot / 2]
@@ -132,18 +133,18 @@ __global__ void __launch_bounds__(kRopeThreads, !kHalf ? 8 : V == 4 && sizeof(T)
       float2 mine[kPairs];
 #pragma unroll
       for (int e = 0; e < kPairs; e++) mine[e] = rotated ? cs[t * pairs + u * kPairs + e] : make_float2(1.f, 0.f);
-      rotate_heads<T, V, kHalf, kPairs>(static_cast<const T*>(a.q) + b * a.qs[0] + n * a.qs[1],
+      rotate_heads<T, V, kHalf, kVector, kPairs>(static_cast<const T*>(a.q) + b * a.qs[0] + n * a.qs[1],
                                                static_cast<T*>(a.qo) + b * a.qos[0] + n * a.qos[1], a.qs[2], a.qos[2],
                                                a.Hq, first, rows, pairs, at, rotated, mine);
       if (a.k)
-        rotate_heads<T, V, kHalf, kPairs>(static_cast<const T*>(a.k) + b * a.ks[0] + n * a.ks[1],
+        rotate_heads<T, V, kHalf, kVector, kPairs>(static_cast<const T*>(a.k) + b * a.ks[0] + n * a.ks[1],
                                                  static_cast<T*>(a.ko) + b * a.kos[0] + n * a.kos[1], a.ks[2], a.kos[2],
                                                  a.Hkv, first, rows, pairs, at, rotated, mine);
     }
   }
 }
 
-template <typename T, int V, bool kHalf>
+template <typename T, int V, bool kHalf, bool kVector>
 static cudaError_t go(const RopeArgs& a, cudaStream_t st) {
   const long long tokens = (long long)a.B * a.N;
   const int units = (kHalf ? a.rot / 2 / V : a.rot / V) + (a.d - a.rot) / V;
@@ -153,7 +154,7 @@ static cudaError_t go(const RopeArgs& a, cudaStream_t st) {
   long long tile = tokens < 4 * 592 ? 1 : apart < 4 ? 4 : apart < tokens / 592 ? apart : tokens / 592;
   while (tile > 4 && tile * a.rot / 2 * sizeof(float2) > 16384) tile /= 2;
   const dim3 block(wide, rows * apart);
-  rope_kernel<T, V, kHalf><<<dim3((unsigned)((tokens + tile - 1) / tile)), block, tile * a.rot / 2 * sizeof(float2), st>>>(
+  rope_kernel<T, V, kHalf, kVector><<<dim3((unsigned)((tokens + tile - 1) / tile)), block, tile * a.rot / 2 * sizeof(float2), st>>>(
       a, (int)tile, rows);
   return cudaGetLastError();
 }
@@ -163,12 +164,19 @@ static cudaError_t go_type(const RopeArgs& a, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T), H = V < 4 ? V : 4;
   // wide units need every row and every run of channels to start and end on one
   // (the pointers do); a unit of the half layout is V pairs, so its halves must too
-  const int unit = a.half ? H : V;
-  bool wide = a.d % unit == 0 && a.rot % (a.half ? 2 * H : V) == 0;
-  for (int i = 0; i < 3; i++) wide = wide && a.qs[i] % unit == 0 && (!a.k || a.ks[i] % unit == 0);
-  if (a.half)
-    return wide ? go<T, H, true>(a, st) : go<T, 1, true>(a, st);
-  return wide ? go<T, V, false>(a, st) : go<T, 2, false>(a, st);
+  const auto multiples = [&a](int unit) {
+    bool all = a.d % unit == 0;
+    for (int i = 0; i < 3; i++) all = all && a.qs[i] % unit == 0 && (!a.k || a.ks[i] % unit == 0);
+    return all;
+  };
+  const bool wide = multiples(a.half ? H : V) && a.rot % (a.half ? 2 * H : V) == 0;
+  if (a.half) return wide ? go<T, H, true, true>(a, st) : go<T, 1, true, false>(a, st);
+  if (wide) return go<T, V, false, true>(a, st);
+  // One pair a unit: of fp32 that is 8 bytes, one access if all rows start on 8 bytes (those of dense tensors
+  // do, as d is even); strides may be odd.
+  if constexpr (sizeof(T) == 4)
+    if (multiples(2)) return go<T, 2, false, true>(a, st);
+  return go<T, 2, false, false>(a, st);
 }
 
 cudaError_t launch_rope(const RopeArgs& a, bool bf16, cudaStream_t st) {
