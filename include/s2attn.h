@@ -318,7 +318,8 @@ S2_API size_t s2attn_cache4_workspace_bytes(void);
  * rows t = cu_new[r] .. cu_new[r+1]-1 of q [T][H_q][d] (strides of token and head in elements,
  * multiples of 16 bytes). lens[r] counts the request's stored tokens, those of this step
  * included; its row number i of n sees the first lens[r] - (n - 1 - i): its own place and all
- * before. Query head h uses kv head h / (H_q / H_kv). o is dense [T][H_q][d]; lse, if not
+ * before. table_stride 0: one row of pages for all requests; else at least max_pages. Query head
+ * h uses kv head h / (H_q / H_kv). o is dense [T][H_q][d]; lse, if not
  * NULL, is [H_q][T] float32. A row that sees no key gets o = 0 and lse = -inf; rows that no
  * request owns stay as they were. max_new: the largest number of rows of a request, from
  * which the kernel's tile is chosen (another value costs time, not correctness); so is it from

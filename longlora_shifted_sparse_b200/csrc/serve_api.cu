@@ -228,7 +228,7 @@ s2_status s2attn_cache4_attn(const void* q, const void* cache, const int* block_
   if (!q || !cache || !block_table || !lens || !cu_new || !o || !q_strides) return S2_ERR_NULL;
   if (!dtype_ok(dtype)) return S2_ERR_DTYPE;
   if (R <= 0 || T <= 0 || H_q <= 0 || H_kv <= 0 || H_q % H_kv || H_q > 65535 || max_pages <= 0 ||
-      table_stride < max_pages || max_new <= 0 || (long long)T * H_q > 0x7fffffffLL ||
+      (table_stride != 0 && table_stride < max_pages) || max_new <= 0 || (long long)T * H_q > 0x7fffffffLL ||
       !cache_ok(n_pages, page_size))
     return S2_ERR_SHAPE;
   if (!headdim32_ok(d)) return S2_ERR_HEADDIM;

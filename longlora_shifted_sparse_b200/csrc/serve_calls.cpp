@@ -33,12 +33,14 @@ bool ints(const Tensor* t, int device, int64_t count) {
          (count < 0 || t->numel() == count);
 }
 
-// A block table of R requests: dense rows.
-bool table_ok(const Tensor* t, int device, int64_t R) {
+// A block table of R requests: dense rows that do not overlap or, where they are only read, all the same row.
+bool table_ok(const Tensor* t, int device, int64_t R, bool one_row) {
   return t && t->scalar_type() == at::kInt && here(*t, device) && t->dim() == 2 && t->size(0) == R && R > 0 &&
-         t->size(1) > 0 && t->size(1) <= INT_MAX && (t->size(1) == 1 || t->stride(1) == 1);
+         t->size(1) > 0 && t->size(1) <= INT_MAX && (t->size(1) == 1 || t->stride(1) == 1) &&
+         (R == 1 || t->stride(0) >= t->size(1) || (one_row && t->stride(0) == 0));
 }
-long long table_stride(const Tensor& t) { return std::max<int64_t>(t.stride(0), t.size(1)); }
+// (The stride of a single row says nothing.)
+long long table_stride(const Tensor& t) { return t.size(0) == 1 ? t.size(1) : t.stride(0); }
 
 struct Cache {
   int pages, page, heads, d;
@@ -142,7 +144,7 @@ PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!ints(cached, device, -1) || !number(a[5], page) || !number(a[6], T) || T < 0 || T > INT_MAX - 4) Py_RETURN_NONE;
   const int64_t R = cached->numel();
   if (R > 4096 || !ints(fresh, device, R) || !ints(free, device, -1) || free->numel() > INT_MAX || !ints(count, device, 1) ||
-      !table_ok(table, device, R))
+      !table_ok(table, device, R, false))
     Py_RETURN_NONE;
   const int64_t rows = (T + 3) & ~3LL;  // positions and slots on 16 bytes
   const Tensor out = at::empty({2 * rows + 2 * R + 3}, cached->options());
@@ -209,7 +211,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int dt = code_of(q->scalar_type());
   float scale = c.d > 0 ? (float)std::pow((double)c.d, -0.5) : 0.f;
   if (dt < 0 || q->size(2) != c.d || T == 0 || T > INT_MAX || Hq > INT_MAX || R > INT_MAX - 1 || !ints(cu, device, R + 1) ||
-      !table_ok(table, device, R) || (a[6] != Py_None && !number(a[6], scale)) || !ws || !here(*ws, device) || ws->dim() != 1 ||
+      !table_ok(table, device, R, true) || (a[6] != Py_None && !number(a[6], scale)) || !ws || !here(*ws, device) || ws->dim() != 1 ||
       ws->scalar_type() != at::kByte || !ws->is_contiguous() ||
       (!given && a[8] != Py_None))
     Py_RETURN_NONE;

@@ -365,13 +365,14 @@ def _ints(t, name, device, shape=None):
 
 
 def _table(t, device, R):
-    """Columns and row stride of a block table of R requests."""
+    """Columns and row stride of a block table of R requests. Rows may all be one (stride 0), as in a
+    table that is expanded over requests which share their pages; a caller that writes refuses that."""
     if t.dtype is not _i32:
         raise TypeError("block_table must be int32, got %s" % t.dtype)
     shape = t.shape
     if len(shape) != 2 or shape[0] != R or t.device != device or (shape[1] > 1 and t.stride(1) != 1):
         raise ValueError("block_table must be [R, max_pages] on %s with dense rows" % device)
-    return shape[1], max(t.stride(0), shape[1])
+    return shape[1], shape[1] if R == 1 else t.stride(0)
 
 
 def _dense_like(x):
@@ -540,7 +541,7 @@ def page_plan(cached_lens, new_lens, free_pages, free_count, block_table, page_s
     Returns cu_new [R+1], lens [R] (cached + new), positions and slots [max_tokens] (slots -1
     in rows that no request owns), free_count [1] (what is left) and left_out [1]: the number
     of requests that did not fit (too long for the table or for max_tokens, or no pages left),
-    whose slots are -1 and whose lengths stay."""
+    whose slots are -1 and whose lengths stay. The rows of block_table must not overlap."""
     out = _plain("page_plan", cached_lens, new_lens, free_pages, free_count, block_table, page_size, max_tokens)
     if out is not None:
         return tuple.__new__(PagePlan, out)
@@ -549,6 +550,7 @@ def page_plan(cached_lens, new_lens, free_pages, free_count, block_table, page_s
     c, n = _ints(cached_lens, "cached_lens", dev, (R,)), _ints(new_lens, "new_lens", dev, (R,))
     f, fc = _ints(free_pages, "free_pages", dev), _ints(free_count, "free_count", dev, (1,))
     cols, stride = _table(block_table, dev, R)
+    _need(stride >= cols, "block_table is written: its rows must not overlap")
     rows = (max_tokens + 3) & ~3   # positions and slots on 16 bytes
     out = torch.empty(2 * rows + 2 * R + 3, dtype=_i32, device=dev)
     p = out.data_ptr()
@@ -636,7 +638,7 @@ def cache4_attention(q, cache, block_table, lens, cu_new, max_new: int, scale=No
     """Attention of a step's tokens over all that the cache holds of their requests.
 
     q [T, Hq, d]; request r has its rows cu_new[r] .. cu_new[r+1]-1 (int32 [R+1]), the pages
-    block_table[r] (int32 [R, max_pages]) and lens[r] stored tokens, those of this step
+    block_table[r] (int32 [R, max_pages]; an expanded row serves requests that share all pages) and lens[r] stored tokens, those of this step
     included (int32 [R]); a row sees its own place and all before. max_new: the largest number
     of rows of a request (known to the caller; it picks the kernel's tile). scale: 1 / sqrt(d)
     by default. ws: ``cache4_workspace``, made anew where it is None. Returns o [T, Hq, d] (out, if
@@ -656,6 +658,8 @@ def cache4_attention(q, cache, block_table, lens, cu_new, max_new: int, scale=No
     dt, R = _dtype_code(q), lens.numel()
     ln, cu = _ints(lens, "lens", dev, (R,)), _ints(cu_new, "cu_new", dev, (R + 1,))
     cols, stride = _table(block_table, dev, R)
+    if 0 < stride < cols:   # rows that overlap
+        block_table, stride = block_table.contiguous(), cols
     q, qs = _cache4_rows(q)
     if out is None:
         out = _dense_like(q)
