@@ -440,6 +440,7 @@ __device__ __forceinline__ void fill(const Cache4AttnArgs& a, Shared& sh, uint32
     cur = next;
     ok = mbar_wait<2>(smem_addr(&sh.kv_empty[g & 1]), ((g >> 1) & 1) ^ 1, ab);
     cp_async_wait_all();
+    __syncwarp();  // the wait is for this lane's copies; a vote would not order the others' before the reads below
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     uint32_t kx[2][NG], sc[2][NG / 2], lo[2][NG / 2], vx[2][NG], pair[2][NG];

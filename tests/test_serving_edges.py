@@ -1,6 +1,8 @@
 """Calls of the serving operators that their documentation allows and that ordinary use seldom makes: odd strides, shared and
 overlapping tensors, infinities, numbers that do not fit."""
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -110,3 +112,23 @@ def test_requests_that_share_pages(s2, R, dtype, d, new):
         seen = lens.clamp(max=windows.shape[1] * P)
         args = (seen, cu, new)
         assert torch.equal(s2.cache4_attention(q, cache, windows, *args), s2.cache4_attention(q, cache, windows.clone().contiguous(), *args))
+
+
+# --------------------------------------------------------------------------------- kernels' sources
+
+def test_waits_for_own_copies_are_followed_by_a_barrier():
+    """A thread's wait for its asynchronous copies says nothing of other threads' copies, nor does a vote: a barrier of the warp or
+    block stands between the wait and whatever the kernel does next with shared memory (or the function ends)."""
+    root = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "longlora_shifted_sparse_b200", "csrc")
+    waits = 0
+    for name in ("cache4_attn.cu", "cache4_tc.cu", "cache4_simt.cu"):
+        with open(os.path.join(root, name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        for m in re.finditer(r"(cp_async_wait_all\(\);|cp_async_wait<[^>]*>\(\);|\"cp\.async\.wait_all;\")", text):
+            waits += 1
+            rest = text[m.end():]
+            barrier = re.search(r"__syncwarp\(\)|__syncthreads\(\)|\n}", rest)
+            between = rest[:barrier.start()]
+            # sums over lanes into places of their own (the few-row kernel's maxima and sums) read nothing that was copied
+            assert not re.search(r"ld_shared|load_words|__all_sync|__any_sync|copy\(|issue\(", between), (name, between)
+    assert waits == 5
