@@ -18,7 +18,9 @@
 // holds it (bf16 has fewer bits; what is lost is below 2^-29 of the row's largest channel);
 // the power returns in the scores' factor.
 // v codes become values minimum + scale * code in fp16, half a step (2^-11) off, and so do the
-// probabilities: both well below the output's bf16. Maxima, sums and accumulators are fp32.
+// probabilities: both well below the output's bf16. The probabilities are 2^15 at the running maximum, near
+// the top of fp16, so that those of 2^-29 of it still have all their bits and only those below 2^-40 are dropped: many
+// small ones may be the whole output, where the largest ones' values are zero. Maxima, sums and accumulators are fp32.
 //
 // Work is steps of 32 keys of a (request, kv head, tile). All steps of the call lie on one line
 // and each CTA takes an equal run of them, whatever the requests' lengths, or, of short calls, one
@@ -45,6 +47,7 @@ namespace s2 {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kStep = 32;  // keys of a step
+constexpr float kUp = 15.f;  // log2 of a probability at the maximum
 constexpr int kTries = 4, kCutChunk = 128;
 __device__ constexpr int kMore[kTries] = {0, 2, 5, 10};  // steps
 
@@ -550,8 +553,9 @@ __global__ void __launch_bounds__(kThreads, MINB) cache4_attn_kernel(const __gri
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
           t = fmaxf(t, m[nt][e]);
           grew |= t > m[nt][e];
-          top[e] = t == -INFINITY ? 0.f : t;
-          alpha[nt][e] = ex2(m[nt][e] - top[e]);
+          const float base = t == -INFINITY ? 0.f : t;
+          alpha[nt][e] = ex2(m[nt][e] - base);
+          top[e] = base - kUp;
           m[nt][e] = t;
         }
 #pragma unroll
@@ -677,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, MINB) cache4_attn_kernel(const __gri
           *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) +
                                     ((size_t)(rq.row0 + i) * a.Hq + hq) * d + col) = out;
           if (a.lse && col == 0)
-            a.lse[(size_t)hq * a.T + rq.row0 + i] = L == 0.f ? -INFINITY : (top + log2f(L)) * 0.6931471805599453f;
+            a.lse[(size_t)hq * a.T + rq.row0 + i] = L == 0.f ? -INFINITY : (top - kUp + log2f(L)) * 0.6931471805599453f;
         } else {
           *reinterpret_cast<float4*>(part_o + row * d + col) = sum;
           if (col == 0) {
@@ -728,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, MINB) cache4_attn_kernel(const __gri
           *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) +
                                     ((size_t)(rq.row0 + i) * a.Hq + hq) * d + col) = out;
           if (a.lse && col == 0)
-            a.lse[(size_t)hq * a.T + rq.row0 + i] = L == 0.f ? -INFINITY : (top + log2f(L)) * 0.6931471805599453f;
+            a.lse[(size_t)hq * a.T + rq.row0 + i] = L == 0.f ? -INFINITY : (top - kUp + log2f(L)) * 0.6931471805599453f;
         }
       }
     }

@@ -20,8 +20,8 @@
 //   warps 12..19  softmax and O, a thread a row (TMEM lane).
 // fp16 holds k and v to half a step 2^-11 of the value (the codes are 4 bits wide) and P to 2^-11
 // of itself, below the output's bf16 (2^-8); scores, maxima, sums and O are fp32.
-// The running maximum is kept as an integer 4 below the row's first ones (P then uses fp16's range)
-// and moves only when a sum of P shows that some P might leave that range, so that the common
+// The running maximum is kept as an integer 8 below the row's first ones (P then uses fp16's range: it is
+// dropped below 2^-33 of them) and moves only when a sum of P shows that some P might leave that range, so that the common
 // step takes no maximum and O is rescaled, exactly, a few times a row.
 //
 // Work is steps of 128 keys, laid on one line over (request, kv head, tile) with the steps that the
@@ -54,7 +54,9 @@ constexpr int kFill0 = 4, kFillWarps = 8, kSoft0 = 12, kThreads = 640;
 constexpr int kRegsIssue = 40, kRegsFill = 88, kRegsSoftmax = 128;
 static_assert(kRegsIssue + 2 * kRegsFill + 2 * kRegsSoftmax <= 5 * 96, "register split exceeds the launch allocation");
 constexpr uint32_t kTmemCols = 512;
-constexpr float kBelow = 4.f, kGrow = 5.f;    // log2 units
+// log2 units. A P of a new maximum is at most 2^kBelow, so that 64 of them stay within kSumLimit, and where their sum
+// does not, the largest is above 2^kGrow: the maximum moves.
+constexpr float kBelow = 8.f, kGrow = 9.f;
 constexpr float kSumLimit = 60000.f;          // no P of such a sum overflows fp16
 
 template <int D>

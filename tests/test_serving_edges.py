@@ -8,8 +8,8 @@ import pytest
 import torch
 
 from tests import serving_reference as ref
-from tests.test_serving import BF16, F32, filled, ints, normal, rope_bound
-from tests.test_serving_many import wide
+from tests.test_serving import BF16, F32, HALF, filled, ints, normal, rope_bound
+from tests.test_serving_many import launches, wide
 
 
 @pytest.fixture(scope="module")
@@ -132,3 +132,35 @@ def test_waits_for_own_copies_are_followed_by_a_barrier():
             # sums over lanes into places of their own (the few-row kernel's maxima and sums) read nothing that was copied
             assert not re.search(r"ld_shared|load_words|__all_sync|__any_sync|copy\(|issue\(", between), (name, between)
     assert waits == 5
+
+
+# --------------------------------------------------------------------------------- attention
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("below", [26.3, 31.0])
+@pytest.mark.parametrize("dtype,d,new,kernel", [(BF16, 64, 1, "cache4_attn"), (BF16, 128, 3, "cache4_attn"), (BF16, 256, 1, "cache4_attn"),
+                                                (BF16, 64, 80, "cache4_tc"), (BF16, 128, 70, "cache4_tc"), (F32, 96, 1, "cache4_attn_simt")])
+def test_a_tail_of_small_weights_counts(s2, dtype, d, new, kernel, below):
+    """Every 32nd key is far above the others and has v = 0, so that the output is all made of weights 2^-below of the largest.
+    A weight may be off by half a step of fp16 (2^-11 of it) and, subnormal, by 2^-40 of the largest with few rows, 2^-33 with many."""
+    L, H, P, Hq = 4000, 1, 64, 2
+    a = math.sqrt(below * math.log(2) / (d * d ** -0.5))
+    k, v = torch.full((L, H, d), 0.4 / below * a, device="cuda"), 1 + 0.1 * normal(1, L, H, d)   # (0.4: no whole power of two)
+    k[::32], v[::32] = (1 + 0.4 / below) * a, 0.0
+    k, v = k.to(dtype), v.to(dtype)
+    q = torch.full((new, Hq, d), a, device="cuda").to(dtype)
+    cache = s2.cache4(L // P + 1, P, H, d)
+    s2.cache4_append(k, v, cache, torch.arange(L, dtype=torch.int32, device="cuda"))
+    table = torch.arange(L // P + 1, device="cuda", dtype=torch.int32).view(1, -1)
+    (o, lse), n = launches(s2, kernel, lambda: s2.cache4_attention(q, cache, wide(table), ints([L]), ints([0, new]), new, return_lse=True))
+    assert n == 1
+    kd, vd = ref.quantised(k)[0], ref.quantised(v)[0]
+    want, wl, pv = ref.attention(q, kd, vd, [L - (new - 1 - i) for i in range(new)], d ** -0.5)
+    score = (q.double().abs().sum(-1) * kd.abs().amax() * d ** -0.5).amax()
+    # scores: k in fp16 with many rows (half a step 2^-11), fp32 sums
+    err = score * (2.0 ** -11 if kernel == "cache4_tc" else 2.0 ** -20)
+    most = math.exp(score - wl.min())                       # the largest weight
+    floor = {"cache4_attn": 2.0 ** -40, "cache4_tc": 2.0 ** -33, "cache4_attn_simt": 0.0}[kernel]
+    bound = HALF[dtype] * want.abs() * 1.01 + (3 * 2.0 ** -11 + 2 * err) * pv + floor * most * vd.abs().sum(0).amax()
+    assert (want >= 2.0 ** -30).all() and ((o.double() - want).abs() <= bound).all()
+    assert ((lse.T.double() - wl).abs() <= err + 2.0 ** -20 * (4 + wl.abs())).all()
