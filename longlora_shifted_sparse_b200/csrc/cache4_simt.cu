@@ -71,9 +71,11 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache4_attn_simt_kernel(
   const int* table = a.table + lo * a.table_stride;
 
   // The queries, and apart from them each group's sum; channel x is kept over 16^(x % 4), which code_at's factor undoes.
+  // A row with an infinity has no softmax, and its scores may all be -inf, which marks hidden keys: NaN instead.
   for (int i = threadIdx.x; i < H * d; i += blockDim.x) {
     const int g = i / d, x = i - g * d;
-    q[g][x] = to_f32<T>(static_cast<const T*>(a.q)[t * a.qs[0] + (hq + g) * a.qs[1] + x]) * a.scale;
+    const float y = to_f32<T>(static_cast<const T*>(a.q)[t * a.qs[0] + (hq + g) * a.qs[1] + x]);
+    q[g][x] = fabsf(y) == INFINITY ? NAN : y * a.scale;
   }
   __syncthreads();
   if (threadIdx.x < H * n) {

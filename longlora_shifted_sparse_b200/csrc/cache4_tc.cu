@@ -360,6 +360,8 @@ struct QueryRows {
       const int ex = max((int)(__float_as_uint(big) >> 23), 9);
       float down = __uint_as_float((uint32_t)(262 - ex) << 23);
       down = a.scale < 0.f ? -down : a.scale == 0.f ? 0.f : down;
+      // A row with an infinity has no softmax. Its scores may all be -inf, which marks hidden keys: NaN instead.
+      if (big == INFINITY) down = NAN;
       if (r < kRows) {
         st_shared16(dst + (ch >> 3) * Layout<D>::half + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
                     make_uint4(pack_half2(f[0] * down, f[4] * down), pack_half2(f[1] * down, f[5] * down),

@@ -164,3 +164,36 @@ def test_a_tail_of_small_weights_counts(s2, dtype, d, new, kernel, below):
     bound = HALF[dtype] * want.abs() * 1.01 + (3 * 2.0 ** -11 + 2 * err) * pv + floor * most * vd.abs().sum(0).amax()
     assert (want >= 2.0 ** -30).all() and ((o.double() - want).abs() <= bound).all()
     assert ((lse.T.double() - wl).abs() <= err + 2.0 ** -20 * (4 + wl.abs())).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,new,kernel", [(BF16, 64, 1, "cache4_attn"), (BF16, 128, 3, "cache4_attn"), (BF16, 64, 70, "cache4_tc"),
+                                                (BF16, 128, 64, "cache4_tc"), (F32, 96, 2, "cache4_attn_simt"), (BF16, 32, 2, "cache4_attn_simt")])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("inf", [math.inf, -math.inf])
+def test_an_infinite_query_spoils_its_row(s2, inf, sign, dtype, d, new, kernel):
+    """Every score of such a row is infinite, here of one sign: the softmax of the row is NaN where it sees a key, whichever kernel
+    runs, and 0 where it sees none; other rows are as they were."""
+    L, H, P, Hq = 66, 1, 16, 2
+    k, v = sign * (1 + 0.1 * normal(1, L, H, d).abs()).to(dtype), normal(2, L, H, d).to(dtype)
+    q = normal(3, new, Hq, d).to(dtype)
+    cache = s2.cache4(L // P + 1, P, H, d)
+    s2.cache4_append(k, v, cache, torch.arange(L, dtype=torch.int32, device="cuda"))
+    table = wide(torch.arange(L // P + 1, device="cuda", dtype=torch.int32).view(1, -1))
+    for held in (L, new, 1, 0):
+        args = (cache, table, ints([held]), ints([0, new]), new)
+        good, good_l = s2.cache4_attention(q, *args, return_lse=True)
+        bad, row = q.clone(), new - 1
+        bad[row, 1, 7] = inf
+        if new > 1:
+            bad[0, 0] = inf                     # sees held - (new - 1) keys: none, one or more
+        (o, lse), n = launches(s2, kernel, lambda: s2.cache4_attention(bad, *args, return_lse=True))
+        assert n == 1
+        spoilt = {(row, 1): held} | ({(0, 0): max(0, held - (new - 1))} if new > 1 else {})
+        for (i, h), keys in spoilt.items():
+            if keys:
+                assert o[i, h].isnan().all() and lse[h, i].isnan()
+            else:
+                assert (o[i, h] == 0).all() and lse[h, i] == -math.inf
+            o[i, h], lse[h, i] = good[i, h], good_l[h, i]
+        assert torch.equal(o, good) and torch.equal(lse, good_l)
