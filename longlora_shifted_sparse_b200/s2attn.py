@@ -310,7 +310,7 @@ _torch = None
 
 def _lazy():
     """torch and the compiled calls, imported on the first call, with the names that every call needs."""
-    global _torch, _calls, _device_now, _raw_stream, _i32, _DTYPES
+    global _torch, _calls, _device_now, _raw_stream, _i32, _DTYPES, _forward_ad
     import torch
     if not os.path.exists(CALLS_PATH):
         raise ImportError("_serve_calls.so is not built (expected at %s); build it with "
@@ -322,6 +322,7 @@ def _lazy():
     spec.loader.exec_module(_calls)
     _device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _i32, _DTYPES = torch.int32, {torch.bfloat16: S2_BF16, torch.float32: S2_FP32}
+    _forward_ad = torch.autograd.forward_ad
     _torch = torch
     return torch
 
@@ -476,24 +477,35 @@ def _overlaps(x) -> bool:
 _rope_fn = None
 
 
+def _dual() -> bool:
+    """True inside a level of forward-mode differentiation: a tensor may carry a tangent that requires_grad does not show."""
+    return _forward_ad._current_level >= 0
+
+
 def _make_rope_function():
     import torch
 
     class RopeFunction(torch.autograd.Function):
-        """Autograd wrapper: the gradient is the same rotation the other way round."""
+        """Autograd wrapper: the gradient is the same rotation the other way round, a tangent turns as its value."""
 
         @staticmethod
         def forward(ctx, q, k, positions, freqs, layout, mscale, inverse):
             ctx.save_for_backward(positions, freqs)
+            ctx.save_for_forward(positions, freqs)
             ctx.args = (layout, mscale, not inverse)
             return _rope_launch(q, k, positions, freqs, layout, mscale, inverse, False)
 
         @staticmethod
         def backward(ctx, dq, dk):
             call = (dq, dk, *ctx.saved_tensors, *ctx.args)
-            # (the launch itself unless a gradient of the gradient may be asked for)
-            dq, dk = RopeFunction.apply(*call) if torch.is_grad_enabled() else _rope_launch(*call, False)
+            # (the launch itself unless a gradient or tangent of the gradient may be asked for)
+            dq, dk = RopeFunction.apply(*call) if torch.is_grad_enabled() or _dual() else _rope_launch(*call, False)
             return dq, dk, None, None, None, None, None
+
+        @staticmethod
+        def jvp(ctx, tq, tk, *_):
+            layout, mscale, other_way = ctx.args
+            return RopeFunction.apply(tq, tk, *ctx.saved_tensors, layout, mscale, not other_way)
 
     return RopeFunction
 
@@ -505,14 +517,15 @@ def rope(q, k, positions, freqs, layout: str = "interleaved", mscale: float = 1.
     positions: int32 or int64, [N] (or [T]) or [B, N]; freqs: ``rope_freqs``, whose length gives
     the rotated channels, the first 2 * len(freqs); the rest pass through. layout: pair i is
     channels (2i, 2i+1) ("interleaved", as in the attention calls) or (i, i + half)
-    ("half"). mscale multiplies the rotated channels. Differentiable in q and k;
-    in_place=True overwrites them instead and has no gradient. (To capture a training step into a
+    ("half"). mscale multiplies the rotated channels. Differentiable in q and k (both
+    modes); in_place=True overwrites them instead and has no gradient. (To capture a training step into a
     graph, drop eager graphs of the same leaves first: torch's accumulation nodes keep the stream
     that they were made on.)"""
     if layout not in ROPE_LAYOUTS:
         raise ValueError("layout must be one of %s, got %r" % (sorted(ROPE_LAYOUTS), layout))
-    grad = (q.requires_grad or (k is not None and k.requires_grad)) and (_torch or _lazy()).is_grad_enabled()
-    if not grad:
+    _torch or _lazy()
+    grad = (q.requires_grad or (k is not None and k.requires_grad)) and _torch.is_grad_enabled()
+    if not grad and _forward_ad._current_level < 0:   # (_dual(), for a call a token)
         return _rope_launch(q, k, positions, freqs, layout, mscale, False, in_place)
     _need(not in_place, "in_place=True has no gradient")
     global _rope_fn

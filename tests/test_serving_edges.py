@@ -197,3 +197,47 @@ def test_an_infinite_query_spoils_its_row(s2, inf, sign, dtype, d, new, kernel):
                 assert (o[i, h] == 0).all() and lse[h, i] == -math.inf
             o[i, h], lse[h, i] = good[i, h], good_l[h, i]
         assert torch.equal(o, good) and torch.equal(lse, good_l)
+
+
+# --------------------------------------------------------------------------------- rope and autograd
+
+def tangents(s2, q, k, t, u, pos, f):
+    """rope's forward-mode derivatives: of q and k together, of q alone, without k, and of the backward pass."""
+    from torch.autograd import forward_ad as fw
+    with fw.dual_level():
+        out = [fw.unpack_dual(x).tangent for x in s2.rope(fw.make_dual(q, t), fw.make_dual(k, u), pos, f, layout="half", mscale=1.5)]
+        out += [fw.unpack_dual(x).tangent for x in s2.rope(fw.make_dual(q, t), k, pos, f, layout="half", mscale=1.5)]
+        out.append(fw.unpack_dual(s2.rope(fw.make_dual(q, t), None, pos, f, layout="half", mscale=1.5)[0]).tangent)
+        x = fw.make_dual(q.clone().requires_grad_(), t)
+        (g,) = torch.autograd.grad(s2.rope(x, None, pos, f, layout="half", mscale=1.5)[0].square().sum() / 2, x)
+        out.append(fw.unpack_dual(g).tangent)        # R^T R t
+        with pytest.raises(ValueError, match="no gradient"):
+            s2.rope(fw.make_dual(q, t), None, pos, f, in_place=True)
+        assert all(fw.unpack_dual(x).tangent is None for x in s2.rope(q.detach(), k.detach(), pos, f))
+    return out
+
+
+def check_tangents(s2, q, k, t, u, pos, f, theta):
+    out = tangents(s2, q, k, t, u, pos, f)
+    turn = lambda x: ref.rope(x, pos.view(1, -1), theta, "half", 1.5)  # noqa: E731
+    assert not out[3].any()
+    twice = t.double().clone()
+    twice[..., :2 * theta.numel()] *= 1.5 ** 2
+    for got, want in ((out[0], turn(t)), (out[1], turn(u)), (out[2], turn(t)), (out[4], turn(t)), (out[5], twice)):
+        assert (got.double() - want).abs().max() <= 2.0 ** -20 * want.abs().max()      # a few roundings of fp32
+
+
+def test_rope_carries_tangents(s2, monkeypatch):
+    """Forward-mode derivatives are not lost on the way to the launch (a plain form stands in for it here)."""
+    def plain(q, k, pos, f, layout, mscale, inverse, in_place):
+        return tuple(None if x is None else ref.rope(x, pos.view(1, -1), 2 * math.pi * f, layout, mscale, inverse).to(x.dtype) for x in (q, k))
+
+    monkeypatch.setattr(s2, "_rope_launch", plain)
+    q, k, t, u = (torch.randn(1, 5, 2, 16, generator=torch.Generator().manual_seed(s)) for s in range(4))
+    check_tangents(s2, q, k, t, u, torch.arange(5), s2.rope_freqs(12, device="cpu"), ref.freqs(12))
+
+
+@pytest.mark.gpu
+def test_rope_carries_tangents_on_the_gpu(s2):
+    q, k, t, u = (normal(s, 1, 5, 2, 16) for s in range(4))
+    check_tangents(s2, q, k, t, u, torch.arange(5, device="cuda"), s2.rope_freqs(12), ref.freqs(12))
