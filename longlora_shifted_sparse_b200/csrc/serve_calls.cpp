@@ -78,6 +78,11 @@ bool number(PyObject* x, float& v) {
 
 void* stream(int device) { return c10::cuda::getCurrentCUDAStream(device).stream(); }
 
+// Tells autograd that the library wrote this tensor: a backward pass that saved it before then says so.
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject* refused(int status) { return PyLong_FromLong(status); }
 
 PyObject* pair(const Tensor& a, PyObject* b) {
@@ -156,6 +161,7 @@ PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
       static_cast<int*>(table->data_ptr()), cu, cu + R + 1, p, p + rows, cu + 2 * R + 1, (int)R, (int)T, (int)free->numel(),
       (int)table->size(1), table_stride(*table), (int)page, stream(device));
   if (status) return refused(status);
+  written(*table);
   at::AutoDispatchBelowADInplaceOrView plain;  // whole numbers: no views to track
   const int64_t at[6] = {2 * rows, 2 * rows + R + 1, 0, rows, 2 * rows + 2 * R + 1, 2 * rows + 2 * R + 2};
   const int64_t len[6] = {R + 1, R, T, T, 1, 1};
@@ -176,8 +182,10 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       k->size(1) != c.heads || k->size(2) != c.d || k->size(0) == 0 || k->size(0) > INT_MAX || !ints(slots, device, k->size(0)))
     Py_RETURN_NONE;
   const long long ks[2] = {k->stride(0), k->stride(1)}, vs[2] = {v->stride(0), v->stride(1)};
-  return refused(s2attn_cache4_append(k->data_ptr(), v->data_ptr(), cache->data_ptr(), static_cast<const int*>(slots->data_ptr()),
-                                      (int)k->size(0), c.heads, c.d, c.pages, c.page, ks, vs, dt, stream(device)));
+  const int status = s2attn_cache4_append(k->data_ptr(), v->data_ptr(), cache->data_ptr(), static_cast<const int*>(slots->data_ptr()),
+                                          (int)k->size(0), c.heads, c.d, c.pages, c.page, ks, vs, dt, stream(device));
+  if (status == S2_OK) written(*cache);
+  return refused(status);
 }
 
 // read(cache, slots, code) -> (k, v)
@@ -228,6 +236,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       (int)T, (int)Hq, c.heads, c.d, c.pages, c.page, (int)table->size(1), table_stride(*table), qs, (int)max_new, scale, dt,
       ws->data_ptr(), ws->numel(), stream(device));
   if (status) return refused(status);
+  if (given) written(*given);
   PyObject* out = given ? Py_NewRef(a[8]) : THPVariable_Wrap(o);
   if (!with_lse) return out;
   PyObject* t = PyTuple_New(2);

@@ -350,6 +350,11 @@ def _call(device, fn, *args) -> None:
         raise S2Error(status)
 
 
+def _written(*tensors) -> None:
+    """Tells autograd that the library wrote these tensors: a backward pass that saved one before then says so."""
+    _torch.autograd.graph.increment_version([t for t in tensors if t is not None and not t.is_inference()])
+
+
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
@@ -460,6 +465,8 @@ def _rope_launch(q, k, positions, freqs, layout, mscale, inverse, in_place):
         _call(dev, s2attn_rope, q4.data_ptr(), out.data_ptr(), kp, kop, positions.data_ptr(), wide,
               freqs.data_ptr(), B, N, Hq, Hkv, d, 2 * freqs.shape[0], qst, kst, pst,
               ROPE_LAYOUTS[layout], inverse, mscale, dt)
+        if in_place:
+            _written(q, k)
     return out, kout
 
 
@@ -570,6 +577,7 @@ def page_plan(cached_lens, new_lens, free_pages, free_count, block_table, page_s
     cu = p + 8 * rows
     _call(dev, s2attn_page_plan, c, n, f, fc, block_table.data_ptr(), cu, cu + 4 * (R + 1), p, p + 4 * rows,
           cu + 4 * (2 * R + 1), R, max_tokens, free_pages.numel(), cols, stride, page_size)
+    _written(block_table)
     pos, slots, cu, lens, left, out_of = out.split_with_sizes((rows, rows, R + 1, R, 1, 1))
     if rows != max_tokens:
         pos, slots = pos[:max_tokens], slots[:max_tokens]
@@ -620,6 +628,7 @@ def cache4_append(k, v, cache, slots) -> None:
         v, vs = _cache4_rows(v)
         _call(dev, s2attn_cache4_append, k.data_ptr(), v.data_ptr(), cache.data_ptr(), at, T, Hkv, d,
               n_pages, P, ks, vs, dt)
+        _written(cache)
 
 
 def cache4_read(cache, slots, dtype=None):
@@ -674,6 +683,7 @@ def cache4_attention(q, cache, block_table, lens, cu_new, max_new: int, scale=No
     if 0 < stride < cols:   # rows that overlap
         block_table, stride = block_table.contiguous(), cols
     q, qs = _cache4_rows(q)
+    given = out
     if out is None:
         out = _dense_like(q)
     else:
@@ -686,4 +696,5 @@ def cache4_attention(q, cache, block_table, lens, cu_new, max_new: int, scale=No
               out.data_ptr(), None if lse is None else lse.data_ptr(), R, T, Hq, Hkv, d, n_pages, P,
               cols, stride, qs, max_new, d ** -0.5 if scale is None else scale, dt, ws.data_ptr(),
               ws.numel())
+        _written(given)
     return (out, lse) if return_lse else out

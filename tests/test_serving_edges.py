@@ -241,3 +241,56 @@ def test_rope_carries_tangents(s2, monkeypatch):
 def test_rope_carries_tangents_on_the_gpu(s2):
     q, k, t, u = (normal(s, 1, 5, 2, 16) for s in range(4))
     check_tangents(s2, q, k, t, u, torch.arange(5, device="cuda"), s2.rope_freqs(12), ref.freqs(12))
+
+
+def test_what_is_overwritten_says_so(s2, monkeypatch):
+    """The version counters that autograd checks saved tensors by move with every call that writes a caller's tensor (the launch
+    itself is left out here)."""
+    monkeypatch.setattr(s2, "_call", lambda *a: None)
+    x = torch.zeros(2, 4, 64)
+    i, cache, ws = torch.zeros(2, dtype=torch.int32), s2.cache4(2, 16, 4, 64, device="cpu"), torch.zeros(8, dtype=torch.uint8)
+    table, cu = torch.zeros(2, 1, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    q, k, out = x.clone(), x.clone(), x.clone()
+    f = s2.rope_freqs(64, device="cpu")
+    s2.rope(q, k, i, f, in_place=True)
+    assert (q._version, k._version) == (1, 1)
+    s2.rope(q, None, i, f, in_place=True)
+    s2.rope(q, k, i, f)
+    assert (q._version, k._version) == (2, 1)
+    s2.cache4_append(q, k, cache, i)
+    s2.page_plan(i, i, i, i[:1], table, 16, 4)
+    s2.cache4_attention(x, cache, table, i, cu, 1, ws=ws, out=out)
+    s2.cache4_attention(x, cache, table, i, cu, 1, ws=ws)
+    assert (cache._version, table._version, out._version) == (1, 1, 1)
+    assert (x._version, i._version, q._version, k._version) == (0, 0, 2, 1)
+    with torch.inference_mode():
+        y = torch.zeros(2, 4, 64)
+        s2.rope(y, None, i, f, in_place=True)
+    s2.rope(y, None, i, f, in_place=True)               # (tensors of inference mode have no counter)
+
+
+@pytest.mark.gpu
+def test_a_backward_over_what_was_overwritten_says_so(s2):
+    f, pos = s2.rope_freqs(64), ints([0, 1])
+    cache, table, _ = filled(s2, [40], 16, 2, 64, 1)
+    args = (cache, table, ints([40]), ints([0, 2]), 2)
+    w = torch.ones(2, 4, 64, device="cuda", requires_grad=True)
+
+    def over(write):
+        x = normal(1, 2, 4, 64)
+        y = (x * w).sum()                                # saves x
+        write(x)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+
+    over(lambda x: s2.rope(x, None, pos, f, in_place=True))
+    over(lambda x: s2.cache4_attention(normal(2, 2, 4, 64), *args, out=x))
+    over(lambda x: s2.cache4_attention(normal(2, 2, 4, 128)[..., 1:65], *args, out=x))    # rows off 16 bytes: the Python path
+    was = cache._version, table._version
+    s2.cache4_append(normal(3, 1, 2, 64), normal(4, 1, 2, 64), cache, ints([5]))
+    s2.page_plan(ints([0]), ints([1]), ints([0]), ints([1]), table, 16, 1)
+    assert (cache._version, table._version) == (was[0] + 1, was[1] + 1)
+    with torch.inference_mode():
+        x = normal(1, 2, 4, 64)
+    s2.rope(x, None, pos, f, in_place=True)
+    s2.cache4_attention(normal(2, 2, 4, 64), *args, out=x)
