@@ -461,6 +461,7 @@ def _rope_launch(q, k, positions, freqs, layout, mscale, inverse, in_place):
     if in_place:
         _need(same, "in place needs dense, 16-byte aligned channels")
         _need(all(not _overlaps(x) for x in (q, k) if x is not None), "in place needs rows that do not overlap")
+        _need(k is None or not _meet(q, k), "in place needs q and k that do not overlap")
     if B * N * (Hq + Hkv):
         _call(dev, s2attn_rope, q4.data_ptr(), out.data_ptr(), kp, kop, positions.data_ptr(), wide,
               freqs.data_ptr(), B, N, Hq, Hkv, d, 2 * freqs.shape[0], qst, kst, pst,
@@ -479,6 +480,43 @@ def _overlaps(x) -> bool:
                 return True
             reach += (size - 1) * stride
     return False
+
+
+def _meet(x, y) -> bool:
+    """True where an element of x and one of y (of one type, neither overlapping itself) may share an address."""
+    size, apart = x.element_size(), y.data_ptr() - x.data_ptr()
+    if x.is_contiguous() and y.is_contiguous():
+        return -size * y.numel() < apart < size * x.numel() and x.numel() > 0 < y.numel()
+    if x.numel() == 0 or y.numel() == 0:
+        return False
+    return apart % size != 0 or _meet_at(x.shape, x.stride(), y.shape, y.stride(), apart // size)
+
+
+@functools.lru_cache(maxsize=4096)
+def _meet_at(x_shape, x_strides, y_shape, y_strides, apart) -> bool:
+    """The same by shapes and strides, y beginning `apart` elements behind x."""
+    # Some sum of a_s * s over the strides s has to be `apart`: a_s runs from minus y's places along s to x's.
+    reach = {}
+    for shape, steps, way, end in ((x_shape, x_strides, 1, 1), (y_shape, y_strides, -1, 0)):
+        for n, s in zip(shape, steps):
+            if n > 1:
+                reach.setdefault(s, [0, 0])[end] += way * (n - 1)
+    strides = sorted(reach, reverse=True)
+    tries = 0
+
+    def found(i, left):
+        nonlocal tries
+        tries += 1
+        if tries > 10000:   # (strides of no order: taken to overlap)
+            return True
+        if i == len(strides):
+            return left == 0
+        s, (low, high) = strides[i], reach[strides[i]]
+        down = sum(reach[r][0] * r for r in strides[i + 1:])
+        up = sum(reach[r][1] * r for r in strides[i + 1:])
+        return any(found(i + 1, left - a * s) for a in range(max(low, -((up - left) // s)), min(high, (left - down) // s) + 1))
+
+    return found(0, apart)
 
 
 _rope_fn = None
@@ -525,7 +563,7 @@ def rope(q, k, positions, freqs, layout: str = "interleaved", mscale: float = 1.
     the rotated channels, the first 2 * len(freqs); the rest pass through. layout: pair i is
     channels (2i, 2i+1) ("interleaved", as in the attention calls) or (i, i + half)
     ("half"). mscale multiplies the rotated channels. Differentiable in q and k (both
-    modes); in_place=True overwrites them instead and has no gradient. (To capture a training step into a
+    modes); in_place=True overwrites them (they must not overlap) instead and has no gradient. (To capture a training step into a
     graph, drop eager graphs of the same leaves first: torch's accumulation nodes keep the stream
     that they were made on.)"""
     if layout not in ROPE_LAYOUTS:

@@ -294,3 +294,41 @@ def test_a_backward_over_what_was_overwritten_says_so(s2):
         x = normal(1, 2, 4, 64)
     s2.rope(x, None, pos, f, in_place=True)
     s2.cache4_attention(normal(2, 2, 4, 64), *args, out=x)
+
+
+def addresses(t):
+    at = torch.full(t.shape, t.data_ptr() // t.element_size())
+    for i, (n, s) in enumerate(zip(t.shape, t.stride())):
+        at += (s * torch.arange(n)).view([-1 if i == j else 1 for j in range(t.dim())])
+    return set(at.flatten().tolist())
+
+
+def test_rope_in_place_refuses_what_would_turn_twice(s2, monkeypatch):
+    """q and k that share an element would both write it. Rows that only interleave, as those of one projection do, are taken."""
+    monkeypatch.setattr(s2, "_call", lambda *a: None)
+    f, pos, buf = s2.rope_freqs(4, device="cpu"), torch.arange(64), torch.zeros(4000)
+    g = torch.Generator().manual_seed(0)
+    pick = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))  # noqa: E731
+    met = 0
+    for _ in range(600):
+        B, T, d, heads = pick(1, 3), pick(1, 5), 4 * pick(1, 2), (pick(1, 4), pick(1, 4))
+        hs = d + 4 * pick(0, 3)
+        ts = 4 * hs + 4 * pick(0, 20)
+        bs = T * ts + 4 * pick(0, 9)
+        if pick(0, 3) == 0:                                # head-major
+            hs, ts = T * hs, hs
+            bs = max(bs, 4 * hs)
+        q, k = (buf.as_strided((B, T, h, d), (bs, ts, hs, 1), 4 * pick(0, 80)) for h in heads)
+        if addresses(q) & addresses(k):
+            met += 1
+            with pytest.raises(ValueError, match="overlap"):
+                s2.rope(q, k, pos[:T], f, in_place=True)
+        else:
+            s2.rope(q, k, pos[:T], f, in_place=True)
+    assert 100 < met < 500
+    x = torch.zeros(2, 3, 2, 8)
+    for q, k in ((x, x), (x, x[:, :, :1]), (x[:, :, :2], x.view(2, 3, 2, 8)[:, :, 1:])):
+        with pytest.raises(ValueError, match="overlap"):
+            s2.rope(q, k, pos[:3], f, in_place=True)
+    s2.rope(x[:, :, :1], x[:, :, 1:], pos[:3], f, in_place=True)
+    s2.rope(x, x, pos[:3], f)                              # (outputs of their own)
