@@ -305,21 +305,13 @@ def s2_attention(q, k, v, G: int, pi_scale: float, rope_base: float = 10000.0,
 # leaves every other case, and what to say about it, to the code here.
 
 CALLS_PATH = os.path.join(_HERE, "_serve_calls.so")
-_torch = None
+_torch = _calls = None
 
 
 def _lazy():
-    """torch and the compiled calls, imported on the first call, with the names that every call needs."""
-    global _torch, _calls, _device_now, _raw_stream, _i32, _DTYPES, _forward_ad
+    """torch, imported on the first call, with the names that every call needs."""
+    global _torch, _device_now, _raw_stream, _i32, _DTYPES, _forward_ad
     import torch
-    if not os.path.exists(CALLS_PATH):
-        raise ImportError("_serve_calls.so is not built (expected at %s); build it with "
-                          "`python -m longlora_shifted_sparse_b200.build`" % CALLS_PATH)
-    from importlib import machinery, util
-    spec = util.spec_from_file_location("_serve_calls", CALLS_PATH,
-                                        loader=machinery.ExtensionFileLoader("_serve_calls", CALLS_PATH))
-    _calls = util.module_from_spec(spec)
-    spec.loader.exec_module(_calls)
     _device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _i32, _DTYPES = torch.int32, {torch.bfloat16: S2_BF16, torch.float32: S2_FP32}
     _forward_ad = torch.autograd.forward_ad
@@ -327,10 +319,25 @@ def _lazy():
     return torch
 
 
+def _load_calls():
+    """The compiled serving calls, loaded on the first of them (the training calls do without)."""
+    global _calls
+    _torch or _lazy()
+    if not os.path.exists(CALLS_PATH):
+        raise ImportError("_serve_calls.so is not built (expected at %s); build it with "
+                          "`python -m longlora_shifted_sparse_b200.build`" % CALLS_PATH)
+    from importlib import machinery, util
+    spec = util.spec_from_file_location("_serve_calls", CALLS_PATH,
+                                        loader=machinery.ExtensionFileLoader("_serve_calls", CALLS_PATH))
+    calls = util.module_from_spec(spec)
+    spec.loader.exec_module(calls)
+    _calls = calls
+
+
 def _plain(call, *args):
     """What a compiled call returns: outputs, or None where the case is not the plain one."""
-    if _torch is None:
-        _lazy()
+    if _calls is None:
+        _load_calls()
     if not args[0].is_cuda:   # (before any CUDA call: there may be no device)
         return None
     out = getattr(_calls, call)(*args)

@@ -1,8 +1,10 @@
 """Calls of the serving operators that their documentation allows and that ordinary use seldom makes: odd strides, shared and
 overlapping tensors, infinities, numbers that do not fit."""
+import importlib.util
 import math
 import os
 import re
+import shutil
 
 import pytest
 import torch
@@ -332,3 +334,19 @@ def test_rope_in_place_refuses_what_would_turn_twice(s2, monkeypatch):
             s2.rope(q, k, pos[:3], f, in_place=True)
     s2.rope(x[:, :, :1], x[:, :, 1:], pos[:3], f, in_place=True)
     s2.rope(x, x, pos[:3], f)                              # (outputs of their own)
+
+
+# --------------------------------------------------------------------------------- what is built
+
+def test_training_calls_do_without_the_compiled_serving_calls(s2, tmp_path):
+    package = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "longlora_shifted_sparse_b200")
+    for name in ("s2attn.py", "libs2attn.so"):
+        shutil.copy(os.path.join(package, name), tmp_path / name)
+    spec = importlib.util.spec_from_file_location("s2attn_alone", tmp_path / "s2attn.py")
+    alone = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(alone)
+    x, alone._stream_ptr = torch.zeros(1, 3, 2, 64), lambda device: 0
+    with pytest.raises(alone.S2Error, match="invalid shape"):      # the library's own refusal of the group size
+        alone.forward(x, x, x, 2, 1.0)
+    with pytest.raises(ImportError, match="not built"):
+        alone.cache4_append(x[0], x[0], x, x)
