@@ -3,7 +3,7 @@
 Each ``csrc/*.cu`` compiles to an object under ``_build/`` (rebuilt when it or a header is
 newer), then nvcc links the shared library with the CUDA runtime linked statically. The torch
 layer's serving calls (``csrc/serve_calls.cpp``) compile to ``_serve_calls.so`` beside it, against
-torch's headers.
+torch's headers; without torch there is no torch layer, and the library alone is built.
 """
 from __future__ import annotations
 
@@ -70,12 +70,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     return LIB
 
 
-def build_calls(force: bool = False, verbose: bool = False) -> str:
+def build_calls(force: bool = False, verbose: bool = False) -> str | None:
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
     src, header = os.path.join(CSRC, "serve_calls.cpp"), os.path.join(ROOT, "include", "s2attn.h")
     if not force and os.path.exists(CALLS) and \
             os.path.getmtime(CALLS) >= max(os.path.getmtime(src), os.path.getmtime(header)):
         return CALLS
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch = spec.submodule_search_locations[0]
     include = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
                os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"],

@@ -350,3 +350,11 @@ def test_training_calls_do_without_the_compiled_serving_calls(s2, tmp_path):
         alone.forward(x, x, x, 2, 1.0)
     with pytest.raises(ImportError, match="not built"):
         alone.cache4_append(x[0], x[0], x, x)
+
+
+def test_the_library_is_built_without_torch(s2, monkeypatch):
+    from longlora_shifted_sparse_b200 import build
+    find = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
+    assert build.build() == build.LIB
+    assert build.build_calls(force=True) is None       # and makes no attempt
