@@ -736,6 +736,7 @@ def cache4_attention(q, cache, block_table, lens, cu_new, max_new: int, scale=No
               out.is_contiguous(), "out must be a dense tensor like q")
     lse = _torch.empty((Hq, T), dtype=_torch.float32, device=dev) if return_lse else None
     _need(ws.device == dev, "ws is on %s, not on %s" % (ws.device, dev))
+    _need(ws.dtype is _torch.uint8 and ws.is_contiguous(), "ws must be a tensor that cache4_workspace() made")
     if T:
         _call(dev, s2attn_cache4_attn, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), ln, cu,
               out.data_ptr(), None if lse is None else lse.data_ptr(), R, T, Hq, Hkv, d, n_pages, P,

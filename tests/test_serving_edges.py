@@ -358,3 +358,18 @@ def test_the_library_is_built_without_torch(s2, monkeypatch):
     monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
     assert build.build() == build.LIB
     assert build.build_calls(force=True) is None       # and makes no attempt
+
+
+def test_a_workspace_is_dense_bytes(s2, monkeypatch):
+    """Its number of elements is taken for its size: a tensor that repeats its elements would be shorter than it says."""
+    launched = []
+    monkeypatch.setattr(s2, "_call", lambda *a: launched.append(a))
+    i, cache, x = torch.zeros(1, dtype=torch.int32), s2.cache4(2, 16, 4, 64, device="cpu"), torch.zeros(1, 4, 64)
+    size = s2.s2attn_cache4_workspace_bytes()
+    attend = lambda ws: s2.cache4_attention(x, cache, i.view(1, 1), i, torch.zeros(2, dtype=torch.int32), 1, ws=ws)  # noqa: E731
+    for bad in (torch.zeros(1, dtype=torch.uint8).expand(size), torch.zeros(16, 2, dtype=torch.uint8)[:, 0], torch.zeros(size // 4, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="workspace"):
+            attend(bad)
+    assert not launched
+    attend(s2.cache4_workspace("cpu"))
+    assert len(launched) == 1
