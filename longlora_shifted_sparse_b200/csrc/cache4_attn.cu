@@ -751,7 +751,8 @@ cudaError_t go(Cache4AttnArgs a, cudaStream_t st) {
   // no more CTAs than the longest lengths the table allows can occupy, a run of min_chunk each
   const long long tiles = ((long long)a.max_new * (a.Hq / a.Hkv) + 8 * NT - 1) / (8 * NT);
   const long long steps = (((long long)a.max_pages << a.page_shift) + kStep - 1) / kStep;
-  const long long parts = (long long)a.R * a.Hkv * tiles * ((steps + a.min_chunk - 1) / a.min_chunk);
+  // (a double: max_new is only a hint and may be anything)
+  const double parts = (double)a.R * a.Hkv * tiles * ((steps + a.min_chunk - 1) / a.min_chunk);
   a.roomy = parts <= 148 * MINB;
   const int ctas = a.roomy ? (int)parts : 148 * MINB;
   kernel<<<ctas, kThreads, sizeof(S), st>>>(a);

@@ -373,3 +373,22 @@ def test_a_workspace_is_dense_bytes(s2, monkeypatch):
     assert not launched
     attend(s2.cache4_workspace("cpu"))
     assert len(launched) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("columns", [1, (2 ** 31 - 256) // 256])
+def test_the_hint_may_be_anything(s2, columns):
+    """The largest hint and the widest table together (their product with the requests and heads is beyond 64 bits)."""
+    R, H, P, d = 4096, 32, 256, 256
+    cache, one, _ = filled(s2, [40], P, H, d, 1)
+    table = (one if columns == 1 else wide(one, columns)).expand(R, -1)
+    q = normal(2, 5, H, d, dtype=BF16)
+    cu = torch.full((R + 1,), 5, dtype=torch.int32, device="cuda")       # requests 0 and 7 have rows, the others none
+    cu[0], cu[1:8] = 0, 2
+    lens = torch.full((R,), 40, dtype=torch.int32, device="cuda")
+    few = s2.cache4_attention(q, cache, one.expand(2, -1), ints([40, 40]), ints([0, 2, 5]), 3)
+    assert few.isfinite().all()
+    for said in (2 ** 31 - 1, 3):
+        got = s2.cache4_attention(q, cache, table, lens, cu, said)
+        # tiles of 8 or 16 rows: other orders of the same sums
+        assert (got.float() - few.float()).abs().max() <= 2.0 ** -7 * few.float().abs().max()
