@@ -321,7 +321,8 @@ S2_API size_t s2attn_cache4_workspace_bytes(void);
  * before. table_stride 0: one row of pages for all requests; else at least max_pages. Query head
  * h uses kv head h / (H_q / H_kv). o is dense [T][H_q][d]; lse, if not
  * NULL, is [H_q][T] float32. A row that sees no key gets o = 0 and lse = -inf; rows that no
- * request owns stay as they were. max_new: the largest number of rows of a request, from
+ * request owns, or one whose rows do not all lie within q, stay as they were (cu_new must not
+ * decrease). max_new: the largest number of rows of a request, from
  * which the kernel's tile is chosen (another value costs time, not correctness); so is it from
  * R and max_pages, which bound the work. A page number outside the cache among those a row attends
  * to makes that row NaN; lens beyond max_pages * page_size (at most 2^31 - 256) counts as that

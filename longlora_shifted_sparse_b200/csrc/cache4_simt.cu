@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache4_attn_simt_kernel(
   const int t = blockIdx.x, hq = blockIdx.y * H, d = a.d, n = d / 32;
   const int h = hq / (a.Hq / a.Hkv);
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  // the request of token t: rows that no request owns stay as they are
+  // the request of token t: rows that no request owns, or one whose rows leave q, stay as they are
   int lo = 0, hi = a.R;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache4_attn_simt_kernel(
       hi = mid;
   }
   const int begin = a.cu[lo], end = a.cu[lo + 1];
-  if (t < begin || t >= end) return;
+  if (begin < 0 || t < begin || t >= end || end > a.T) return;
   const long long held = min((long long)max(a.lens[lo], 0), (long long)a.max_pages << a.page_shift);
   const int keys = (int)max(0LL, held - (end - 1 - t));  // keys 0 .. keys - 1 are seen
   // this CTA's keys

@@ -709,8 +709,8 @@ def cache4_attention(q, cache, block_table, lens, cu_new, max_new: int, scale=No
     included (int32 [R]); a row sees its own place and all before. max_new: the largest number
     of rows of a request (known to the caller; it picks the kernel's tile). scale: 1 / sqrt(d)
     by default. ws: ``cache4_workspace``, made anew where it is None. Returns o [T, Hq, d] (out, if
-    given, which must not overlap q), or (o, lse) with lse [Hq, T]; rows that no request owns are
-    not written. There is no gradient. A row that sees no key gets 0 and -inf. ``device_status(ws)`` reads whether a wait inside
+    given, which must not overlap q), or (o, lse) with lse [Hq, T]; rows that no request owns, or one
+    whose rows do not all lie within q, are not written. There is no gradient. A row that sees no key gets 0 and -inf. ``device_status(ws)`` reads whether a wait inside
     the call expired."""
     if ws is None:
         ws = cache4_workspace(q.device)

@@ -392,3 +392,18 @@ def test_the_hint_may_be_anything(s2, columns):
         got = s2.cache4_attention(q, cache, table, lens, cu, said)
         # tiles of 8 or 16 rows: other orders of the same sums
         assert (got.float() - few.float()).abs().max() <= 2.0 ** -7 * few.float().abs().max()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,columns", [(BF16, 64, 0), (BF16, 256, 0), (BF16, 128, 1 << 15), (F32, 64, 0), (F32, 96, 1 << 15), (BF16, 32, 0)])
+def test_a_request_whose_rows_leave_the_buffer(s2, dtype, d, columns):
+    """page_plan leaves a request out whose tokens do not fit the step and still counts its rows: the attention writes none of them."""
+    cache, table, _ = filled(s2, [90, 120, 40], 16, 2, d, 3)
+    if columns:
+        table = wide(table, columns)
+    q, out = normal(1, 70, 4, d, dtype=dtype), torch.full((70, 4, d), 7.0, dtype=dtype, device="cuda")
+    lens, cu = ints([90, 120, 40]), [0, 66, 66 + 40, 66 + 41]
+    o = s2.cache4_attention(q, cache, table, lens, ints(cu), 66, out=out)
+    want = s2.cache4_attention(q[:66], cache, table[:1], lens[:1], ints([0, 66]), 66)
+    assert o.data_ptr() == out.data_ptr() and (o[66:] == 7.0).all()
+    assert (o[:66].float() - want.float()).abs().max() <= 2.0 ** -7 * want.float().abs().max()     # (other cuts of the same sums)
