@@ -274,7 +274,8 @@ S2_API s2_status s2attn_rope(const void* q, void* q_out, const void* k, void* k_
  * A request is left out (its slots are -1, lens[r] = cached_lens[r], it takes no page) where a
  * length is negative, max_pages columns do not hold it, its rows do not end within T, or the
  * free pages do not suffice; with the last two, so is every later request that has rows or
- * takes pages. Outputs other than block_table must not alias inputs. */
+ * takes pages. A page number that is negative, or whose slots pass 2^31, gives slots of -1.
+ * Outputs other than block_table must not alias inputs. */
 S2_API s2_status s2attn_page_plan(const int* cached_lens, const int* new_lens,
                                   const int* free_pages, const int* free_count, int* block_table,
                                   int* cu_new, int* lens, int* positions, int* slots, int* counts,

@@ -148,10 +148,11 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
         const int held = (c + (1 << a.page_shift) - 1) >> a.page_shift;
         const int p = col < held ? a.table[r * a.table_stride + col]
                                  : a.free_pages[free_count - 1 - (page[r] + col - held)];
-        base = (int)((unsigned)p << a.page_shift);
+        // a page whose slots have no 31-bit number is none: -1, not another page's slots
+        base = (unsigned)p <= 0x7fffffffu >> a.page_shift ? p << a.page_shift : -1;
         last = col;
       }
-      slot[e] = base + (pos[e] & ((1 << a.page_shift) - 1));
+      if (base >= 0) slot[e] = base + (pos[e] & ((1 << a.page_shift) - 1));
     }
     if (E == 4 && wide && t0 + 4 <= a.T) {
       *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[E > 1], pos[E > 2 ? 2 : 0], pos[E - 1]);

@@ -407,3 +407,31 @@ def test_a_request_whose_rows_leave_the_buffer(s2, dtype, d, columns):
     want = s2.cache4_attention(q[:66], cache, table[:1], lens[:1], ints([0, 66]), 66)
     assert o.data_ptr() == out.data_ptr() and (o[66:] == 7.0).all()
     assert (o[:66].float() - want.float()).abs().max() <= 2.0 ** -7 * want.float().abs().max()     # (other cuts of the same sums)
+
+
+# --------------------------------------------------------------------------------- plans
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens", [80, 148 * 256 + 1])
+@pytest.mark.parametrize("page", [-1, -2 ** 27, -2 ** 28, 2 ** 27, 2 ** 28 + 3, 2 ** 31 - 1, -2 ** 31, 2 ** 27 - 1])
+def test_plans_with_pages_that_are_none(s2, page, tokens):
+    """A page number that no slot can have gives slots of -1, and not those of another page by its low bits: 2^28 pages of 16 tokens
+    are 2^32 slots. The last page whose slots have numbers is taken."""
+    P, n = 16, tokens // 2
+    table = torch.zeros(2, -(-n // P) + 1, dtype=torch.int32, device="cuda")
+    free = torch.arange(5, 5 + 2 * table.shape[1], dtype=torch.int32, device="cuda")
+    free[-2] = page                                   # the first request's second page
+    table[1, 0] = page                                # the second request's first, held already
+    p = s2.page_plan(ints([0, 10]), ints([n, n - 10]), free, ints([free.numel()]), table, P, 2 * n)
+    count = free.numel()
+    slots = p.slots.tolist()
+    last = page == 2 ** 27 - 1
+    want = [(-1 if page_no == page and not last else page_no * P + i % P)
+            for i in range(n) for page_no in [free[count - 1 - i // P].item()]] if n < 1000 else None
+    assert slots[16:32] == ([page * P + i for i in range(16)] if last else [-1] * 16)
+    assert slots[n:n + 6] == ([page * P + i for i in range(10, 16)] if last else [-1] * 6)
+    if want:
+        assert slots[:n] == want
+    rest = p.slots[32:n].tolist() + p.slots[n + 6:2 * n - 10].tolist()
+    assert all(5 * P <= x < (5 + count) * P for x in rest + slots[:16]) and len(set(rest)) == len(rest)
+    assert p.left_out.tolist() == [0]
