@@ -18,9 +18,10 @@
 // holds it (bf16 has fewer bits; what is lost is below 2^-29 of the row's largest channel);
 // the power returns in the scores' factor.
 // v codes become values minimum + scale * code in fp16, half a step (2^-11) off, and so do the
-// probabilities: both well below the output's bf16. The probabilities are 2^15 at the running maximum, near
-// the top of fp16, so that those of 2^-29 of it still have all their bits and only those below 2^-40 are dropped: many
-// small ones may be the whole output, where the largest ones' values are zero. Maxima, sums and accumulators are fp32.
+// probabilities: both well below the output's bf16. The probabilities are multiplied by 2^15 first, so that the
+// largest lie near the top of fp16, those of 2^-29 still have all their bits and only those below 2^-40 are dropped: many
+// small ones may be the whole output, where the largest ones' values are zero. (As a smaller maximum, without the products,
+// the 15 would be lost in the rounding of scores beyond 2^24.) Maxima, sums and accumulators are fp32.
 //
 // Work is steps of 32 keys of a (request, kv head, tile). All steps of the call lie on one line
 // and each CTA takes an equal run of them, whatever the requests' lengths, or, of short calls, one
@@ -47,7 +48,7 @@ namespace s2 {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kStep = 32;  // keys of a step
-constexpr float kUp = 15.f;  // log2 of a probability at the maximum
+constexpr float kUp = 0x1p15f;  // of the probabilities as operands, and so of the accumulators
 constexpr int kTries = 4, kCutChunk = 128;
 __device__ constexpr int kMore[kTries] = {0, 2, 5, 10};  // steps
 
@@ -553,17 +554,16 @@ __global__ void __launch_bounds__(kThreads, MINB) cache4_attn_kernel(const __gri
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
           t = fmaxf(t, m[nt][e]);
           grew |= t > m[nt][e];
-          const float base = t == -INFINITY ? 0.f : t;
-          alpha[nt][e] = ex2(m[nt][e] - base);
-          top[e] = base - kUp;
+          top[e] = t == -INFINITY ? 0.f : t;
+          alpha[nt][e] = ex2(m[nt][e] - top[e]);
           m[nt][e] = t;
         }
 #pragma unroll
         for (int mt = 0; mt < 2; mt++) {
 #pragma unroll
           for (int e = 0; e < 4; e++) S[mt][nt][e] = ex2(S[mt][nt][e] - top[e & 1]);
-          P[mt][nt][0] = transpose8(pack_half2(S[mt][nt][0], S[mt][nt][1]));
-          P[mt][nt][1] = transpose8(pack_half2(S[mt][nt][2], S[mt][nt][3]));
+          P[mt][nt][0] = transpose8(pack_half2(S[mt][nt][0] * kUp, S[mt][nt][1] * kUp));
+          P[mt][nt][1] = transpose8(pack_half2(S[mt][nt][2] * kUp, S[mt][nt][3] * kUp));
         }
 #pragma unroll
         for (int e = 0; e < 2; e++)
@@ -675,13 +675,13 @@ __global__ void __launch_bounds__(kThreads, MINB) cache4_attn_kernel(const __gri
         }
         if (starts && ends) {
           const int full = tile * ROWS + row, i = full / group, hq = h * group + full - i * group;
-          const float inv = L == 0.f ? 0.f : 1.f / L;
+          const float inv = L == 0.f ? 0.f : 1.f / (L * kUp);
           const uint2 out = make_uint2(sm100::pack_bf16x2(sum.x * inv, sum.y * inv),
                                        sm100::pack_bf16x2(sum.z * inv, sum.w * inv));
           *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) +
                                     ((size_t)(rq.row0 + i) * a.Hq + hq) * d + col) = out;
           if (a.lse && col == 0)
-            a.lse[(size_t)hq * a.T + rq.row0 + i] = L == 0.f ? -INFINITY : (top - kUp + log2f(L)) * 0.6931471805599453f;
+            a.lse[(size_t)hq * a.T + rq.row0 + i] = L == 0.f ? -INFINITY : (top + log2f(L)) * 0.6931471805599453f;
         } else {
           *reinterpret_cast<float4*>(part_o + row * d + col) = sum;
           if (col == 0) {
@@ -726,13 +726,13 @@ __global__ void __launch_bounds__(kThreads, MINB) cache4_attn_kernel(const __gri
             M = Mn;
           }
           const int full = tile * ROWS + row, i = full / group, hq = h * group + full - i * group;
-          const float inv = L == 0.f ? 0.f : 1.f / L, top = M == -INFINITY ? 0.f : M;
+          const float inv = L == 0.f ? 0.f : 1.f / (L * kUp), top = M == -INFINITY ? 0.f : M;
           const uint2 out = make_uint2(sm100::pack_bf16x2(sum.x * inv, sum.y * inv),
                                        sm100::pack_bf16x2(sum.z * inv, sum.w * inv));
           *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) +
                                     ((size_t)(rq.row0 + i) * a.Hq + hq) * d + col) = out;
           if (a.lse && col == 0)
-            a.lse[(size_t)hq * a.T + rq.row0 + i] = L == 0.f ? -INFINITY : (top - kUp + log2f(L)) * 0.6931471805599453f;
+            a.lse[(size_t)hq * a.T + rq.row0 + i] = L == 0.f ? -INFINITY : (top + log2f(L)) * 0.6931471805599453f;
         }
       }
     }

@@ -435,3 +435,35 @@ def test_plans_with_pages_that_are_none(s2, page, tokens):
     rest = p.slots[32:n].tolist() + p.slots[n + 6:2 * n - 10].tolist()
     assert all(5 * P <= x < (5 + count) * P for x in rest + slots[:16]) and len(set(rest)) == len(rest)
     assert p.left_out.tolist() == [0]
+
+
+LARGE_SCORES = [(BF16, 64, 1, "cache4_attn"), (BF16, 128, 3, "cache4_attn"), (BF16, 256, 2, "cache4_attn"), (F32, 96, 2, "cache4_attn_simt")]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,new,kernel", LARGE_SCORES)
+@pytest.mark.parametrize("power", [16, 20, 22, 23, 24, 25, 26, 27, 30, 60])
+def test_large_scores(s2, power, dtype, d, new, kernel):
+    """Scores of 2^power and some times it, where fp32 rounds to whole numbers and more: the softmax is the value of the largest."""
+    L, H, P, Hq = 200, 1, 16, 2
+    k, v = normal(power, L, H, d).to(dtype), normal(2, L, H, d).to(dtype)
+    k[::2] = 0.0                                            # scores that are exactly 0
+    cache = s2.cache4(L // P + 1, P, H, d)
+    s2.cache4_append(k, v, cache, torch.arange(L, dtype=torch.int32, device="cuda"))
+    table = wide(torch.arange(L // P + 1, device="cuda", dtype=torch.int32).view(1, -1))
+    q = (normal(3, new, Hq, d) * 2.0 ** power).to(dtype)
+    kd, vd = ref.quantised(k)[0], ref.quantised(v)[0]
+    hidden = torch.arange(L, device="cuda") >= torch.tensor([L - (new - 1 - i) for i in range(new)], device="cuda").view(-1, 1, 1)
+    for sign in (1, -1):
+        sc = sign * d ** -0.5
+        (o, lse), n = launches(s2, kernel, lambda: s2.cache4_attention(q, cache, table, ints([L]), ints([0, new]), new, scale=sc, return_lse=True))
+        assert n == 1 and o.isfinite().all()
+        score = sc * torch.einsum("nhd,ld->nhl", q.double(), kd[:, 0])
+        top, at = score.masked_fill(hidden, -math.inf).topk(2, -1)
+        # k in fp16 with many rows (half a step 2^-11 of each product), fp32 sums otherwise
+        off = abs(sc) * torch.einsum("nhd,ld->nhl", q.double().abs(), kd[:, 0].abs()).amax(-1) * (2.0 ** -11 if kernel == "cache4_tc" else 2.0 ** -20)
+        clear = top[..., 0] - top[..., 1] > 2 * off + 40   # the others' weights are below 2^-50 together
+        assert clear.double().mean() > 0.5
+        want = vd[at[..., 0], 0]
+        assert ((o.double() - want).abs() <= (HALF[dtype] + 2.0 ** -10) * want.abs())[clear].all()       # v in fp16, and the output
+        assert ((lse.T.double() - top[..., 0]).abs() <= off + 2.0 ** -20 * top[..., 0].abs() + 0.7).all()   # (two equal ones: log 2)
