@@ -442,11 +442,8 @@ __device__ __forceinline__ void fill(const Cache4AttnArgs& a, Shared& sh, uint32
     if (!has_prev && !has_cur) break;
     prev = cur;
     cur = next;
-    ok = mbar_wait<2>(smem_addr(&sh.kv_empty[g & 1]), ((g >> 1) & 1) ^ 1, ab);
     cp_async_wait_all();
     __syncwarp();  // the wait is for this lane's copies; a vote would not order the others' before the reads below
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
     uint32_t kx[2][NG], sc[2][NG / 2], lo[2][NG / 2], vx[2][NG], pair[2][NG];
 #pragma unroll
     for (int it = 0; it < 2; it++) {
@@ -461,6 +458,8 @@ __device__ __forceinline__ void fill(const Cache4AttnArgs& a, Shared& sh, uint32
     if (has_next) copy(next.src, raw_k);
     if (has_cur && cur.src) copy(cur.src + c4::vc_at(D), raw_v);
     cp_async_commit();
+    ok = __all_sync(0xffffffffu, mbar_wait<2>(smem_addr(&sh.kv_empty[g & 1]), ((g >> 1) & 1) ^ 1, ab));
+    if (!ok) break;
     if (has_prev) {
       const uint32_t dst = smem + L::v + ((g - 1) & 1) * L::tile;
 #pragma unroll
