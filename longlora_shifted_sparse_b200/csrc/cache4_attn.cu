@@ -562,8 +562,12 @@ __global__ void __launch_bounds__(kThreads, MINB) cache4_attn_kernel(const __gri
         for (int mt = 0; mt < 2; mt++) {
 #pragma unroll
           for (int e = 0; e < 4; e++) S[mt][nt][e] = ex2(S[mt][nt][e] - top[e & 1]);
-          P[mt][nt][0] = transpose8(pack_half2(S[mt][nt][0] * kUp, S[mt][nt][1] * kUp));
-          P[mt][nt][1] = transpose8(pack_half2(S[mt][nt][2] * kUp, S[mt][nt][3] * kUp));
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            float p0, p1;
+            sm100::f2unpack(sm100::fmul2(sm100::f2pack(S[mt][nt][2 * e], S[mt][nt][2 * e + 1]), sm100::f2pack(kUp, kUp)), p0, p1);
+            P[mt][nt][e] = transpose8(pack_half2(p0, p1));
+          }
         }
 #pragma unroll
         for (int e = 0; e < 2; e++)
