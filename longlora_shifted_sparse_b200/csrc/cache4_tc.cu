@@ -58,6 +58,9 @@ constexpr uint32_t kTmemCols = 512;
 // does not, the largest is above 2^kGrow: the maximum moves.
 constexpr float kBelow = 8.f, kGrow = 9.f;
 constexpr float kSumLimit = 60000.f;          // no P of such a sum overflows fp16
+// A maximum of this size or more is taken as it is, and its row goes the long way: 8 below it is no longer a number of its own, and
+// a product that is not rounded before the maximum is taken off would be away from it by more than fp16 spans.
+constexpr float kLarge = 0x1p22f;
 
 template <int D>
 struct Layout {
@@ -235,13 +238,21 @@ __device__ __forceinline__ void hide32(bool cut, int seen, uint32_t (&x)[32]) {
 #pragma unroll
     for (int c = 0; c < 32; c++) x[c] = c < seen ? x[c] : 0xff800000u;
 }
-// P = exp2(S * factor + shift) of 32 scores as 16 fp16 pairs; their sum is added to acc.
+// P = exp2(S * factor + shift) of 32 scores as 16 fp16 pairs; their sum is added to acc. kRound: the product is rounded
+// first, as the maximum's was.
+template <bool kRound>
 __device__ __forceinline__ void p32(const uint32_t (&x)[32], float factor, float shift, uint32_t* pk, uint64_t& acc) {
   const uint64_t f2 = f2pack(factor, factor), s2 = f2pack(shift, shift);
 #pragma unroll
   for (int c = 0; c < 16; c++) {
     float a0, a1;
-    f2unpack(ffma2(f2pack(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), f2, s2), a0, a1);
+    const float s0 = __uint_as_float(x[2 * c]), s1 = __uint_as_float(x[2 * c + 1]);
+    if (kRound) {  // (by intrinsics that are never made one multiply-add)
+      a0 = __fadd_rn(__fmul_rn(s0, factor), shift);
+      a1 = __fadd_rn(__fmul_rn(s1, factor), shift);
+    } else {
+      f2unpack(ffma2(f2pack(s0, s1), f2, s2), a0, a1);
+    }
     const float p0 = ex2(a0), p1 = ex2(a1);
     acc = fadd2(acc, f2pack(p0, p1));
     pk[c] = pack_half2(p0, p1);
@@ -283,8 +294,9 @@ __device__ __forceinline__ float p_anew(uint32_t tS, int done, bool cut, int see
 #pragma unroll
     for (int e = 0; e < 32; e += 2) top = fmax3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
   }
-  top *= factor;
-  const float mnew = top > m + kGrow ? ceilf(top) - kBelow : m;
+  top = __fmul_rn(top, factor);
+  // (their difference is exact where m + kGrow would round)
+  const float mnew = top - m > kGrow ? ceilf(top) - (fabsf(top) < kLarge ? kBelow : 0.f) : m;
   const float alpha = mnew == m ? 1.f : exp2_int(m - mnew);   // (-inf - -inf)
   if (done == 1) {
     scale_p64(tS, alpha);
@@ -299,7 +311,7 @@ __device__ __forceinline__ float p_anew(uint32_t tS, int done, bool cut, int see
       tmem_wait_ld32(x);
       hide32(cut, seen - h * 64 - c * 32, x);
       // a row that has seen no key yet: its scores are all -inf
-      p32(x, factor, mnew == -INFINITY ? 0.f : -mnew, pk + 16 * c, acc);
+      p32<true>(x, factor, mnew == -INFINITY ? 0.f : -mnew, pk + 16 * c, acc);
     }
     tmem_st32(tS + h * 64, pk);
   }
@@ -720,10 +732,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
           tc_fence_after();
           const bool cut = __any_sync(0xffffffffu, seen < kKeys);
           float rs = 0.f, alpha = 1.f;
-          // The common case: every row of the warp has a maximum m, and P with it does not overflow,
-          // which the sum of P shows: no maximum is taken. P goes over the first 32 columns of its half of S.
+          // The common case: every row of the warp has a maximum m (of ordinary size), and P with it does not
+          // overflow, which the sum of P shows: no maximum is taken. P goes over the first 32 columns of its half of S.
           int done = 0;
-          if (__all_sync(0xffffffffu, m > -INFINITY)) {
+          if (__all_sync(0xffffffffu, fabsf(m) < kLarge)) {
             uint32_t x[2][32], pk[32];
             tmem_ld32(tS, x[0]);
 #pragma unroll
@@ -734,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache4_tc_kernel(const __grid_con
                 tmem_wait_ld32(x[c]);
                 if (2 * h + c < 3) tmem_ld32(tS + (2 * h + c + 1) * 32, x[c ^ 1]);
                 hide32(cut, seen - (2 * h + c) * 32, x[c]);
-                p32(x[c], factor, -m, pk + 16 * c, acc);
+                p32<false>(x[c], factor, -m, pk + 16 * c, acc);
               }
               const float sum = both(acc);
               if (done != h || !__all_sync(0xffffffffu, sum <= kSumLimit)) continue;

@@ -437,7 +437,8 @@ def test_plans_with_pages_that_are_none(s2, page, tokens):
     assert p.left_out.tolist() == [0]
 
 
-LARGE_SCORES = [(BF16, 64, 1, "cache4_attn"), (BF16, 128, 3, "cache4_attn"), (BF16, 256, 2, "cache4_attn"), (F32, 96, 2, "cache4_attn_simt")]
+LARGE_SCORES = [(BF16, 64, 1, "cache4_attn"), (BF16, 128, 3, "cache4_attn"), (BF16, 256, 2, "cache4_attn"), (F32, 96, 2, "cache4_attn_simt"),
+                (BF16, 64, 70, "cache4_tc"), (BF16, 128, 64, "cache4_tc")]
 
 
 @pytest.mark.gpu
@@ -467,3 +468,24 @@ def test_large_scores(s2, power, dtype, d, new, kernel):
         want = vd[at[..., 0], 0]
         assert ((o.double() - want).abs() <= (HALF[dtype] + 2.0 ** -10) * want.abs())[clear].all()       # v in fp16, and the output
         assert ((lse.T.double() - top[..., 0]).abs() <= off + 2.0 ** -20 * top[..., 0].abs() + 0.7).all()   # (two equal ones: log 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("first,then", [(0.0, 2.0 ** 24), (2.0 ** 24, 0.0), (2.0 ** 21, 2.0 ** 23), (-2.0 ** 25, 3.0), (2.0 ** 30, -2.0 ** 30)])
+def test_many_rows_whose_scores_change_their_size(s2, first, then):
+    """Scores of one size over the first tiles of keys, of another over the rest: a row's maximum passes from ordinary to large or stays
+    large. The larger ones' value is the result."""
+    L, H, P, d, new = 900, 1, 64, 64, 64
+    k = torch.empty(L, H, d, device="cuda")
+    k[:400], k[400:] = first / 2 ** 20, then / 2 ** 20
+    v = torch.empty(L, H, d, device="cuda")
+    v[:400], v[400:] = 1.0, -2.0
+    cache = s2.cache4(L // P + 1, P, H, d)
+    s2.cache4_append(k, v, cache, torch.arange(L, dtype=torch.int32, device="cuda"))
+    table = wide(torch.arange(L // P + 1, device="cuda", dtype=torch.int32).view(1, -1))
+    q = torch.full((new, 1, d), 2.0 ** 20, device="cuda", dtype=BF16)       # scores: 64 times first, or then
+    o, lse = s2.cache4_attention(q, cache, table, ints([L]), ints([0, new]), new, scale=1.0, return_lse=True)
+    assert (o == (1.0 if first > then else -2.0)).all()
+    count = torch.arange(L - new + 1, L + 1, device="cuda").double() - 400 if then > first else torch.full((new,), 400.0, device="cuda")
+    want = 64 * max(first, then) + count.log()
+    assert ((lse[0].double() - want).abs() <= 2.0 ** -20 * (4 + want.abs())).all()
