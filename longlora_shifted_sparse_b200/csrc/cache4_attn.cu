@@ -434,7 +434,8 @@ __global__ void __launch_bounds__(kThreads, MINB) cache4_attn_kernel(const __gri
       const float h0 = __half2float(__float2half_rn(s0)), h1 = __half2float(__float2half_rn(s1));
       sm.q.sums[nt][lane] = make_uint2(pack_half2(h0, h1), pack_half2(s0 - h0, s1 - h1));
       if (c == 0) {
-        sm.q.factor[nt * 8 + g] = up * a.scale * (1.4426950408889634f * 0x1p24f);
+        // finite: a score of 0 times infinity would be NaN (queries of 2^115 and more)
+        sm.q.factor[nt * 8 + g] = fminf(fmaxf(up * a.scale * (1.4426950408889634f * 0x1p24f), -3.4e38f), 3.4e38f);
         sm.q.keys[nt * 8 + g] = live ? max(0, rq.held - (rq.n - 1 - i)) : see_max;
       }
     }

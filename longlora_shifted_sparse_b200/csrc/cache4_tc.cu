@@ -378,8 +378,8 @@ struct QueryRows {
         st_shared16(dst + (ch >> 3) * Layout<D>::half + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
                     make_uint4(pack_half2(f[0] * down, f[4] * down), pack_half2(f[1] * down, f[5] * down),
                                pack_half2(f[2] * down, f[6] * down), pack_half2(f[3] * down, f[7] * down)));
-        if (ch == 0)  // never 0: a hidden score times it stays -inf
-          factor[r] = fmaxf(__uint_as_float((uint32_t)(ex - 8) << 23) * fabsf(a.scale) * 1.4426950408889634f, 1.2e-38f);
+        if (ch == 0)  // never 0 or infinite: a hidden score times it stays -inf, and one of 0 stays 0
+          factor[r] = fminf(fmaxf(__uint_as_float((uint32_t)(ex - 8) << 23) * fabsf(a.scale) * 1.4426950408889634f, 1.2e-38f), 3.4e38f);
       }
     }
   }

@@ -489,3 +489,33 @@ def test_many_rows_whose_scores_change_their_size(s2, first, then):
     count = torch.arange(L - new + 1, L + 1, device="cuda").double() - 400 if then > first else torch.full((new,), 400.0, device="cuda")
     want = 64 * max(first, then) + count.log()
     assert ((lse[0].double() - want).abs() <= 2.0 ** -20 * (4 + want.abs())).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,new,kernel", LARGE_SCORES)
+@pytest.mark.parametrize("qscale,scale", [(2.0 ** 117, None), (2.0 ** 105, 2.0 ** 11), (2.0 ** 112, -2.0), (2.0 ** -100, 2.0 ** 115), (2.0 ** -120, 2.0 ** 118)])
+def test_scores_near_the_end_of_fp32(s2, qscale, scale, dtype, d, new, kernel):
+    """Queries and scales of any size whose product with the keys is finite: no NaN, also for the scores that are 0 and where the
+    scales alone, taken out of a row, would be infinite or 0."""
+    L, H, P, Hq = 200, 1, 16, 2
+    k, v = normal(1, L, H, d).to(dtype), normal(2, L, H, d).to(dtype)
+    k[::2] = 0.0
+    cache = s2.cache4(L // P + 1, P, H, d)
+    s2.cache4_append(k, v, cache, torch.arange(L, dtype=torch.int32, device="cuda"))
+    table = wide(torch.arange(L // P + 1, device="cuda", dtype=torch.int32).view(1, -1))
+    q = (normal(3, new, Hq, d) * qscale).to(dtype)
+    (o, lse), n = launches(s2, kernel, lambda: s2.cache4_attention(q, cache, table, ints([L]), ints([0, new]), new, scale=scale, return_lse=True))
+    assert n == 1 and o.isfinite().all() and lse.isfinite().all()
+    sc = d ** -0.5 if scale is None else scale
+    kd, vd = ref.quantised(k)[0], ref.quantised(v)[0]
+    keys = [L - (new - 1 - i) for i in range(new)]
+    want, _, pv = ref.attention(q, kd, vd, keys, sc)
+    score = sc * torch.einsum("nhd,ld->nhl", q.double(), kd[:, 0])
+    hidden = torch.arange(L, device="cuda") >= torch.tensor(keys, device="cuda").view(-1, 1, 1)
+    top = score.masked_fill(hidden, -math.inf).topk(2, -1).values
+    off = abs(sc) * torch.einsum("nhd,ld->nhl", q.double().abs(), kd[:, 0].abs()).amax(-1) * (2.0 ** -11 if kernel == "cache4_tc" else 2.0 ** -20)
+    # as in the tests above: one weight is 1, or all scores are known to their rounding
+    clear = (top[..., 0] - top[..., 1] > 2 * off + 40) | (off < 0.1)
+    assert clear.double().mean() > 0.5
+    small = torch.where(off < 0.1, off, torch.zeros_like(off)).unsqueeze(-1)
+    assert ((o.double() - want).abs() <= HALF[dtype] * 1.01 * want.abs() + (3 * 2.0 ** -11 + 4 * small) * pv)[clear].all()
