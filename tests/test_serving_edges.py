@@ -519,3 +519,67 @@ def test_scores_near_the_end_of_fp32(s2, qscale, scale, dtype, d, new, kernel):
     assert clear.double().mean() > 0.5
     small = torch.where(off < 0.1, off, torch.zeros_like(off)).unsqueeze(-1)
     assert ((o.double() - want).abs() <= HALF[dtype] * 1.01 * want.abs() + (3 * 2.0 ** -11 + 4 * small) * pv)[clear].all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,new,Hq,H,d,P", [([1, 16, 100, 257], [1, 1, 1, 1], 4, 2, 64, 32), ([700, 33], [3, 1], 8, 2, 128, 16),
+                                               ([5000], [1], 2, 2, 128, 64), ([900, 40], [2, 5], 4, 1, 256, 16)])
+@pytest.mark.parametrize("shift", [0.0, 6.0])
+def test_scores_and_small_weights_tightly(s2, lens, new, Hq, H, d, P, shift):
+    """The few-row kernel's scores to fp32: products with the codes (0..15) are exact and so are those with the minima's two parts, so
+    that a sum of them is off by 2^-22 of the sum of their sizes; keys far from zero make the minima's part the larger one. Weights
+    are off by half a step of fp16, or by 2^-40 of the largest."""
+    cache, table, kv = filled(s2, lens, P, H, d, 17)
+    if shift:
+        kv = []
+        for r, n in enumerate(lens):
+            k, v = normal(7 * r, n, H, d, dtype=BF16) + shift, normal(7 * r + 1, n, H, d, dtype=BF16)
+            s2.cache4_append(k, v, cache, (table[r].repeat_interleave(P)[:n] * P + torch.arange(n, device="cuda") % P).int())
+            kv.append((ref.quantised(k), ref.quantised(v)))
+    cu = [sum(new[:r]) for r in range(len(new) + 1)]
+    q = normal(3, cu[-1], Hq, d, dtype=BF16)
+    (o, lse), n = launches(s2, "cache4_attn", lambda: s2.cache4_attention(q, cache, table, ints(lens), ints(cu), max(new), return_lse=True))
+    assert n == 1
+    sc = d ** -0.5
+    for r, m in enumerate(new):
+        rows = slice(cu[r], cu[r + 1])
+        (k, ks), (v, _) = kv[r]
+        keys = [max(0, lens[r] - (m - 1 - i)) for i in range(m)]
+        want, wl, pv = ref.attention(q[rows], k, v, keys, sc)
+        g = q[rows].double().abs().view(m, H, Hq // H, d // 32, 32).sum(-1)                # |q| over a group
+        sizes = 15 * ks.double().amax(0) + k.unflatten(-1, (-1, 32)).abs().amax(-1).amax(0)  # codes' part, and the minima's
+        err = sc * 2.0 ** -22 * (g * sizes.view(1, H, 1, -1)).sum(-1).reshape(m, Hq) + 2.0 ** -22 * wl.abs()
+        live = torch.tensor([x > 0 for x in keys], device="cuda")
+        assert ((lse[:, rows].T.double() - wl).abs() <= err + 2.0 ** -21)[live].all()
+        bound = HALF[BF16] * 1.01 * want.abs() + (2 * 2.0 ** -11 + 2 * err.unsqueeze(-1) + 2.0 ** -18) * pv + 2.0 ** -40 * max(keys) * v.abs().max()
+        assert ((o[rows].double() - want).abs() <= bound)[live].all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_codes_at_every_scale(s2, dtype):
+    """Values on, just below and just above the borders of any two codes, for every mantissa that a scale may have: the code is that of
+    the exact division (the nearest, ties to even)."""
+    S = 1024
+    scale = (1024 + torch.arange(S, device="cuda")).double() * 2.0 ** -12          # fp16 numbers from 1/4 to 1/2
+    border = (torch.arange(15, device="cuda").double() + 0.5).view(1, 15) * scale.view(S, 1)
+    step = lambda x, way: torch.nextafter(x.float(), torch.full_like(x, way, dtype=F32)).double()  # noqa: E731
+    if dtype is F32:
+        sets = [border.float().double(), step(border, math.inf), step(border, 0.0), step(step(border, math.inf), math.inf)]
+    else:
+        sets = [border.to(BF16).double()]
+    H = 2
+    for x in sets:
+        # a group: 0, fifteen scales (its maximum), and the fifteen values, twice; its minimum is 0, so that x - minimum is x
+        top = (15 * scale).to(dtype).double().view(S, 1)
+        rows = torch.cat((torch.zeros(S, 1, device="cuda"), top, x, x), -1).to(dtype).view(S, 1, 32).repeat(1, H, 1)
+        cache, slots = s2.cache4(S // 16, 16, H, 32), torch.arange(S, dtype=torch.int32, device="cuda")
+        s2.cache4_append(rows, rows, cache, slots)
+        g = rows.float()
+        held = ((g.amax(-1, keepdim=True) - 0) * (1 / 15)).half().double()
+        if dtype is F32:
+            assert torch.equal(held[:, 0, 0], scale)
+        quotient = g.double() / held                       # 24 bits by 11: a border is hit exactly or missed by more than fp64 rounds
+        want = quotient.round().clamp(0, 15) * held
+        for got in s2.cache4_read(cache, slots, F32):
+            assert torch.equal(got.double(), want)
