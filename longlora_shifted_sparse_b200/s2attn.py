@@ -393,6 +393,12 @@ def _dense_like(x):
     return _torch.empty_like(x) if x.is_contiguous() else _torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
+def _copied(x):
+    """A dense copy of x, on 16 bytes (contiguous() returns x itself where only its address or a stride that
+    nothing steps along is odd)."""
+    return x.clone(memory_format=_torch.contiguous_format)
+
+
 @functools.lru_cache(maxsize=512)
 def _strides(*s):
     return (_ll * len(s))(*s)
@@ -417,7 +423,7 @@ def _rope_rows(x, name):
     tensor is one batch entry)."""
     st = x.stride()
     if st[-1] != 1 or x.data_ptr() % 16:
-        x = x.contiguous()
+        x = _copied(x)
         st = x.stride()
     return x, _strides(st[0], st[1], st[2]) if len(st) == 4 else _strides(0, st[0], st[1])
 
@@ -650,7 +656,7 @@ def _cache4_rows(x):
     """x [T, H, d] with rows of 16-byte pieces, and its strides of token and head."""
     s0, s1, s2 = x.stride()
     if s2 != 1 or (x.data_ptr() | (s0 | s1) * x.element_size()) % 16:
-        x = x.contiguous()
+        x = _copied(x)
         s0, s1, s2 = x.stride()
     return x, _strides(s0, s1)
 

@@ -1,5 +1,6 @@
 """Calls of the serving operators that their documentation allows and that ordinary use seldom makes: odd strides, shared and
 overlapping tensors, infinities, numbers that do not fit."""
+import ctypes
 import importlib.util
 import math
 import os
@@ -583,3 +584,54 @@ def test_codes_at_every_scale(s2, dtype):
         want = quotient.round().clamp(0, 15) * held
         for got in s2.cache4_read(cache, slots, F32):
             assert torch.equal(got.double(), want)
+
+
+# --------------------------------------------------------------------------------- rows that are copied first
+
+def odd_rows():
+    """[T, H, d] tensors that are dense, or all but, and yet not what the kernels read: an address off 16 bytes, and strides that are
+    odd where there is one token, or one head."""
+    flat = torch.arange(2 * 4 * 64 + 9, dtype=F32)
+    yield flat[1:513].view(2, 4, 64)
+    yield flat[:256].view(1, 4, 64).as_strided((1, 4, 64), (257, 64, 1))
+    yield flat.as_strided((1, 1, 64), (65, 65, 1))
+
+
+def test_dense_rows_off_their_alignment_are_copied(s2, monkeypatch):
+    calls = []
+
+    def launch(device, fn, *args):
+        tensors, strides = args[:2], [list(a) for a in args if isinstance(a, ctypes.Array)]
+        calls.append((fn, [p for p in tensors if p], strides))
+
+    monkeypatch.setattr(s2, "_call", launch)
+    ws = s2.cache4_workspace("cpu")
+    for x in odd_rows():
+        T, H, d = x.shape
+        assert x.data_ptr() % 16 or x.stride(0) % 4 or x.stride(1) % 4
+        i, cache = torch.zeros(T, dtype=torch.int32), s2.cache4(2, 16, H, d, device="cpu")
+        s2.cache4_append(x, x, cache, i)
+        s2.cache4_attention(x, cache, i[:1].view(1, 1), i[:1], i.new_zeros(2), 1, ws=ws)
+        for fn, pointers, strides in calls:
+            assert all(p % 16 == 0 for p in pointers) and all(s % 4 == 0 for row in strides for s in row)
+        calls.clear()
+        s2.rope(x, None, i, s2.rope_freqs(d, device="cpu"))
+        assert all(p % 16 == 0 for p in calls[0][1])
+        calls.clear()
+
+
+@pytest.mark.gpu
+def test_dense_rows_off_their_alignment(s2):
+    f = s2.rope_freqs(64)
+    for x in odd_rows():
+        x = torch.arange(1024, dtype=F32, device="cuda").as_strided(x.shape, x.stride(), x.storage_offset())
+        T, H, d = x.shape
+        y, slots = x.clone(memory_format=torch.contiguous_format), torch.arange(T, dtype=torch.int32, device="cuda")
+        one, two = s2.cache4(1, 16, H, d), s2.cache4(1, 16, H, d)
+        s2.cache4_append(x, x, one, slots)
+        s2.cache4_append(y, y, two, slots)
+        assert torch.equal(one, two) and one.any()
+        args = (one, ints([[0]]), ints([T]), ints([0, T]), T)
+        for dtype in (F32, BF16):
+            assert torch.equal(s2.cache4_attention(x.to(dtype) if dtype is BF16 else x, *args), s2.cache4_attention(y.to(dtype), *args))
+        assert torch.equal(s2.rope(x, None, slots, f)[0], s2.rope(y, None, slots, f)[0])
