@@ -29,12 +29,14 @@
 // copies, and meet only at the end of a tile. A tile that several CTAs share is joined by the last of
 // them to arrive, in the order of the runs, so that the bits do not depend on timing.
 //
-// Measured (B200): 102400 tokens, 32 heads on 32 of 128: 119 us, 524 MB, 4.4 TB/s; 24 requests of up to 32768, 64
-// on 8 of 128: 146 us, 653 MB, 4.5 TB/s. The copies alone take 90 us of the 119, the loop without v 92,
-// without three quarters of k 105: what is left over is the extraction of the codes, two logic or
-// permute operations for a code pair on a pipe that takes one every other cycle. Three CTAs an SM
-// with 168 registers did better than four with 128 (127 us); a maximum that is kept (123), shifts
-// as multiplications (128) and e4m3 operands for k's codes (142) did worse.
+// Measured (B200; from one GPU to another times differ by 6%): 102400 tokens, 32 heads on 32 of 128: 119 to 126 us, 524 MB,
+// 4.2 to 4.4 TB/s; 24 requests of up to 32768, 64 on 8 of 128: 151 to 162 us, 653 MB; 13 requests of up to 6001, 5 tokens,
+// 32 on 8 of 64: 29 us, 29 MB. No unit is full: of the first, DRAM gives 64% of the copy rate, the ALU pipe (logic and
+// permutes, which take the codes out of their words) is 59% busy, issue slots 65%. With three warps a scheduler a warp that does not
+// issue waits for the ALU pipe and for its own last result, a third each. The copies alone take 90 us of 119, the loop
+// without v 92, without three quarters of k 105. Three CTAs an SM with 168 registers did better than four with 128
+// (127 us); a maximum that is kept (123), shifts as multiplications (128) and e4m3 operands for k's codes (142) did worse.
+// The third is short of work: 47% of the issue slots, waits for results, pages and the other warps at a tile's two ends.
 #include <math.h>
 
 #include <type_traits>

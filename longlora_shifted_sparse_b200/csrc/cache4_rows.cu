@@ -73,8 +73,8 @@ struct Chunk<float> {
 };
 
 // Codes of eight values, channel i in bits 4 i, of values whose quotients lie within -0.5 .. 15.5.
-// The quotient is (x - m) inv and a step with its residual, which makes it the rounded one (tried for
-// every mantissa of x - m and s).
+// The quotient is (x - m) inv and a step with its residual, which makes it the correctly rounded one, as inv is the correctly
+// rounded reciprocal (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).
 template <typename T>
 __device__ __forceinline__ uint32_t codes8(const Chunk<T>& x, uint64_t minus_m, uint64_t minus_s, uint64_t inv) {
   using namespace sm100;

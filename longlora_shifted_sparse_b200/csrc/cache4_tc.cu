@@ -29,8 +29,8 @@
 // leaves parts (sums and maxima in fp32) that a second launch joins in the order of the runs.
 // Every wait is bounded; on expiry the status word is set and the CTA drains.
 //
-// Measured (B200, 64 heads on 8 of 128, 512 tokens over 32768): 555 us, 980 TFLOP/s; two requests over 16384
-// and 8636: 440 us, 820. What was tried: mma.sync in tiles of 32 rows 2015 us; three dequantising
+// Measured (B200, 64 heads on 8 of 128, 512 tokens over 32768): 575 us, 950 TFLOP/s; two requests over 16384
+// and 8636: 421 to 448 us from one GPU to another, 800 to 850. What was tried: mma.sync in tiles of 32 rows 2015 us; three dequantising
 // warps 735, seven 486 (16 softmax warps), a thread a row without the maximum 440; bulk copies
 // instead of cp.async 467 (4700 cycles to arrive beside the MMAs' operand reads); 16 softmax warps
 // 486; PV in two halves of the keys, the first under the second's softmax, 500. The MMAs of a half step

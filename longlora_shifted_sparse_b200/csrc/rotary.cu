@@ -8,7 +8,7 @@
 //
 // Bound by HBM: one read and one write of q and k. The angle is formed in fp64 and reduced to
 // (-1/2, 1/2] turns before it is rounded, so that far positions lose nothing; sine and cosine
-// are then fp32. They are formed once per (token, pair) of a CTA's tile, in shared memory,
+// are then fp32 (of the turn rounded to fp32: fp32 outputs are 5.1e-8 off, and 4.0e-8 with an fp64 angle). They are formed once per (token, pair) of a CTA's tile, in shared memory,
 // and shared by all heads: fp64 work per token is rot/2 products. A thread keeps the (cos, sin) of its
 // channels over the heads and has one row in flight; eight CTAs an SM then hide the latency better
 // than more rows a thread (32768 tokens, 64 heads of 128 in bf16: 177 us, 6.1 TB/s, against 182 with

@@ -54,11 +54,15 @@ static_assert((size_t)2 * kCache4SimtCtas * 4 * (256 + 2) <= kTcPartsFloats, "th
 bool cache4_mma(int d, int dt) { return dt == S2_BF16 && (d == 64 || d == 128 || d == 256); }
 // Tiles of 256 query rows on tcgen05, or of 8 to 32 on mma.sync? The first dequantise a key once for
 // many rows; the second start sooner. `rows`: of a request and kv head; `pairs`: rows times keys of
-// the whole call, at most what the block table's width allows. us, mma.sync / tcgen05, d = 128:
-//   1 request, 64 heads on 8, 1024 keys:  64 rows 23 / 28, 128 rows 21 / 29, 512 rows 38 / 37
-//   1 request, 64 heads on 8, 4096 keys:  32 rows 28 / 29,  64 rows 34 / 31, 512 rows 68 / 41
-//   8 requests, 32 heads on 32, 4096 keys: 32 rows 97 / 123, 64 rows 145 / 130, 512 rows 763 / 259
-//   1 request, 64 heads on 8, 16384 keys: 64 rows 58 / 49, 512 rows 187 / 76
+// the whole call, at most what the block table's width allows. us, mma.sync / tcgen05, d = 128, in a table as wide as the keys:
+//   1 request, 64 heads on 8, 256 keys:    64 rows 13 / 24, 512 rows 14 / 34
+//   1 request, 64 heads on 8, 1024 keys:   64 rows 20 / 24, 128 rows 19 / 26, 512 rows 31 / 33
+//   1 request, 64 heads on 8, 4096 keys:   32 rows 26 / 26,  64 rows 34 / 27, 512 rows 70 / 36
+//   8 requests, 32 heads on 32, 4096 keys: 32 rows 127 / 143, 64 rows 225 / 147, 512 rows 1524 / 350
+//   1 request, 64 heads on 8, 16384 keys:  64 rows 57 / 45, 512 rows 206 / 72
+// In a table for 102400 tokens the same calls take 15 / 24, 18 / 35; 19 / 24, 24 / 26, 30 / 33; 35 / 25, 35 / 27, 70 / 36; 127 / 143, 224 / 147,
+// 1524 / 351; 57 / 45, 207 / 72, and the rule, which knows the width and not the lengths, takes tcgen05 from 64 rows on: short chunks in
+// wide tables pay for it, at most 35 us where 14 would do.
 bool cache4_many(int d, long long rows, double pairs) {
   return (d == 64 || d == 128) && rows >= 64 && pairs >= 3.0 * (1 << 20);
 }

@@ -576,8 +576,8 @@ def rope(q, k, positions, freqs, layout: str = "interleaved", mscale: float = 1.
     the rotated channels, the first 2 * len(freqs); the rest pass through. layout: pair i is
     channels (2i, 2i+1) ("interleaved", as in the attention calls) or (i, i + half)
     ("half"). mscale multiplies the rotated channels. Differentiable in q and k (both
-    modes); in_place=True overwrites them (they must not overlap) instead and has no gradient. (To capture a training step into a
-    graph, drop eager graphs of the same leaves first: torch's accumulation nodes keep the stream
+    modes); in_place=True overwrites them (they must not overlap) instead and has no gradient. (To
+    capture a training step into a graph, drop eager graphs of the same leaves first: torch's accumulation nodes keep the stream
     that they were made on.)"""
     if layout not in ROPE_LAYOUTS:
         raise ValueError("layout must be one of %s, got %r" % (sorted(ROPE_LAYOUTS), layout))
@@ -711,13 +711,13 @@ def cache4_attention(q, cache, block_table, lens, cu_new, max_new: int, scale=No
     """Attention of a step's tokens over all that the cache holds of their requests.
 
     q [T, Hq, d]; request r has its rows cu_new[r] .. cu_new[r+1]-1 (int32 [R+1]), the pages
-    block_table[r] (int32 [R, max_pages]; an expanded row serves requests that share all pages) and lens[r] stored tokens, those of this step
-    included (int32 [R]); a row sees its own place and all before. max_new: the largest number
+    block_table[r] (int32 [R, max_pages]; an expanded row serves requests that share all pages) and
+    lens[r] stored tokens, those of this step included (int32 [R]); a row sees its own place and all before. max_new: the largest number
     of rows of a request (known to the caller; it picks the kernel's tile). scale: 1 / sqrt(d)
     by default. ws: ``cache4_workspace``, made anew where it is None. Returns o [T, Hq, d] (out, if
     given, which must not overlap q), or (o, lse) with lse [Hq, T]; rows that no request owns, or one
-    whose rows do not all lie within q, are not written. There is no gradient. A row that sees no key gets 0 and -inf. ``device_status(ws)`` reads whether a wait inside
-    the call expired."""
+    whose rows do not all lie within q, are not written. There is no gradient. A row that sees no key
+    gets 0 and -inf. ``device_status(ws)`` reads whether a wait inside the call expired."""
     if ws is None:
         ws = cache4_workspace(q.device)
     plain = _plain("attention", q, cache, block_table, lens, cu_new, max_new, scale, ws, out, return_lse)
